@@ -428,6 +428,110 @@ int32_t tre_plan_tasks(const tre_config* cfg, int32_t num_sms, int32_t smem_per_
 int32_t tre_plan_op_groups(const tre_config* cfg, int32_t num_sms, int32_t smem_per_block,
                            int32_t* out_ranges, int32_t max_groups);
 
+/* ---- operators of the prompt path ------------------------------------------------
+ *
+ * What runs before the first decode step: the prompt's attention over the caches, the
+ * products with the FP4 experts for many rows at once, the residual addition with its
+ * RMS norm, and the quantiser that makes the MXFP4 rows.  They need no engine: plain
+ * functions on caller-owned device memory.  Conventions of all of them:
+ *   - they run on the CURRENT device, enqueue on `stream` and return; every pointer is a
+ *     device pointer of that device unless its name ends in _host;
+ *   - they allocate nothing, keep nothing between calls and may be captured in a CUDA
+ *     graph and replayed; calls on different streams do not share anything unless the
+ *     caller hands them the same workspace;
+ *   - strides are in elements; pointers are 16-byte aligned and row, head and expert
+ *     strides whole 16-byte units (TRE_ERR_INVALID_ARG otherwise);
+ *   - outputs may not overlap inputs unless the call says so;
+ *   - a size of zero rows is a valid call that writes nothing;
+ *   - results do not depend on the order in which blocks run: the same call on the same
+ *     inputs gives the same bits. */
+
+/* Causal attention of packed prompts over their keys and values (bf16 in and out, fp32
+ * scores, softmax and sums).  Sequence i owns query rows [q_offsets[i], q_offsets[i+1])
+ * and key rows [kv_offsets[i], kv_offsets[i+1]); its last query row sees its last key row,
+ * so with nq queries over nk keys row t (0-based in the sequence) sees key rows
+ * s <= nk - nq + t: nk == nq is a whole prompt, nk > nq a chunk behind a cached prefix,
+ * nq == 1 one decode step.
+ *   out[t][h] = sum_s p_s v[h / (Hq / Hkv)][s],  p = softmax_s(scale q[t][h] . k[..][s])
+ * A row that sees no key (nk < nq) is written as zeros.  Rows of `out` that belong to no
+ * sequence are left as they are.  Keys that a row does not see never reach it, whatever
+ * they hold (NaN and infinities included); the probabilities are rounded to bf16 (a
+ * relative error of at most 2^-8 each) for the product with v, their sum is not. */
+typedef struct {
+  int32_t n_q_heads, n_kv_heads, head_dim;   /* Hq % Hkv == 0; head_dim 64 or 128          */
+  int32_t n_seqs;                            /* sequences; 0 = one that owns every row     */
+  int32_t n_q_rows, n_kv_rows;               /* rows of q and out; rows of k and v         */
+  int64_t q_row_stride, q_head_stride;       /* q  [n_q_rows][Hq][D]                       */
+  int64_t k_row_stride, k_head_stride;       /* k  [Hkv][n_kv_rows][D] (the engine's cache
+                                                layout) or [n_kv_rows][Hkv][D]: by strides */
+  int64_t v_row_stride, v_head_stride;
+  int64_t out_row_stride, out_head_stride;
+  float scale;                               /* > 0; 1 / sqrt(D) in the engine's decode    */
+} tre_attention;
+
+/* Bytes of device workspace that tre_prompt_attention needs for `a` on a device of num_sms
+ * SMs (host only; 0 when none).  Few rows over many keys are split along the keys; the
+ * workspace holds the parts until they are joined. */
+tre_status tre_prompt_attention_workspace(const tre_attention* a, int32_t num_sms, size_t* bytes);
+
+/* q_offsets, kv_offsets: device int32[n_seqs + 1], not decreasing (NULL with n_seqs 0).
+ * They are read when the kernel runs, so a captured call follows their contents; entries
+ * outside [0, rows] are clamped to it.  workspace (16-byte aligned, workspace_bytes as
+ * reported above, NULL when 0) holds nothing before or after the call. */
+tre_status tre_prompt_attention(const tre_attention* a, const void* q, const void* k,
+                                const void* v, const int32_t* q_offsets,
+                                const int32_t* kv_offsets, void* out, void* workspace,
+                                size_t workspace_bytes, tre_stream stream);
+
+/* The tensor-core operators bound every wait on the device.  A wait that runs out of time
+ * ends the kernel with its outputs unspecified and records TRE_ERR_DEP_TIMEOUT in a status
+ * word of the device; this call waits for the current device, returns the word and clears
+ * it (0: every operator call so far has finished its work). */
+tre_status tre_ops_status(int32_t* device_status);
+
+/* Element types of the operators' activations and matrices. */
+enum { TRE_BF16 = 0, TRE_F32 = 1 };
+
+/* w [rows][k] (TRE_BF16 or TRE_F32, row stride in elements, k a multiple of 32) to MXFP4
+ * rows, out [rows][round_up(k/2 + k/32, 16)] bytes in the layout of FP4_EXPERTS above
+ * (contiguous rows; the padding is written as zeros).  The scale of 32 weights is the
+ * power of two 2^(floor(log2(max |w|)) - 2) (clamped to 2^-127 below), the OCP
+ * Microscaling choice; each code is the nearest E2M1 number of w / scale, ties to the even
+ * code, magnitudes over 6 as 6.  Zeros keep their sign; a group of zeros has scale byte 0;
+ * a group that holds a NaN or an infinity has scale byte 255 (NaN) and zero codes. */
+tre_status tre_mxfp4_quantize(const void* w, int32_t type, int64_t rows, int64_t k,
+                              int64_t w_row_stride, void* out, tre_stream stream);
+
+/* The inverse: out [rows][k] (TRE_BF16 or TRE_F32, contiguous) = the numbers that MXFP4
+ * rows stand for, exact in both types (6 x 2^126 and more are infinite in both). */
+tre_status tre_mxfp4_dequantize(const void* w, int64_t rows, int64_t k, int32_t type, void* out,
+                                tre_stream stream);
+
+/* Rows of activations times MXFP4 matrices, grouped by expert:
+ *   out[t][n] = sum_k x[t][k] w[e][n][k]   for t in [offsets[e], offsets[e+1])
+ * x [rows][k] bf16 (row stride in elements), w [n_experts][n][pitch(k)] bytes (contiguous),
+ * out [rows][n] (TRE_BF16 or TRE_F32, row stride in elements, any n: its rows need no
+ * alignment beyond the element's).  The decoded weights are exact and the sums fp32; the
+ * activations are not quantised, as in the engine's FP4 decode.
+ *   offsets   device int32[n_experts + 1], not decreasing, read when the kernel runs and
+ *             clamped to [0, rows]; rows outside [offsets[0], offsets[n_experts]) of out
+ *             are left as they are.  NULL with n_experts 1: every row.
+ * k a multiple of 32; scales 2^(byte - 127) with byte 255 as NaN. */
+tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, const void* w,
+                            const int32_t* offsets, int32_t n_experts, int64_t rows, int64_t n,
+                            int64_t k, int32_t out_type, void* out, int64_t out_row_stride,
+                            tre_stream stream);
+
+/* x_out = x + delta (fp32; delta may be NULL: x_out = x), out = bf16(x_out * g * r) with
+ * r = 1 / sqrt(mean(x_out^2) + eps), row by row.  x, x_out fp32 [rows][d], delta
+ * [rows][d] (TRE_BF16 or TRE_F32), gain bf16[d], out bf16 [rows][d]; d a multiple of 8.
+ * x_out may be x itself (the residual stream updated in place) and may be NULL. */
+tre_status tre_add_rmsnorm(const float* x, int64_t x_row_stride, const void* delta,
+                           int32_t delta_type, int64_t delta_row_stride, const void* gain,
+                           float eps, int64_t rows, int64_t d, float* x_out,
+                           int64_t x_out_row_stride, void* out, int64_t out_row_stride,
+                           tre_stream stream);
+
 /* Human-readable text of the last host-side error of this thread. */
 const char* tre_last_error(void);
 

@@ -1,9 +1,9 @@
 """Build the package's native libraries in-tree.
 
 * ``synth/libtre_synth.so`` — the seeded input generator (gcc + OpenMP).
-* ``libtre.so``             — the engine: host planner + C ABI (C++17) and the
-                              persistent sm_100a kernel (nvcc, -gencode
-                              arch=compute_100a,code=sm_100a).
+* ``libtre.so``             — the engine: host planner + C ABI (C++17), the
+                              persistent sm_100a kernel and the prompt operators
+                              (nvcc, -gencode arch=compute_100a,code=sm_100a).
 
 Run ``python -m persistent_tile_pipelined_b200.build``.  nvcc cross-compiles without a
 GPU, so this works on a CPU-only machine.
@@ -11,6 +11,7 @@ GPU, so this works on a CPU-only machine.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,7 +23,9 @@ INCLUDE = os.path.join(ROOT, "include")
 ENGINE_LIB = os.path.join(PKG, "libtre.so")
 SYNTH_LIB = os.path.join(PKG, "synth", "libtre_synth.so")
 
-ENGINE_SOURCES = ["planner.cpp", "tre_api.cu", "engine.cu", "noalloc.cu"]
+ENGINE_SOURCES = ["planner.cpp", "tre_api.cu", "engine.cu", "noalloc.cu",
+                  "prompt_attention.cu", "mxfp4.cu", "mxfp4_matmul.cu", "add_rmsnorm.cu",
+                  "ops_status.cu"]
 
 
 def engine_headers():
@@ -52,6 +55,18 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _included(path: str, seen=None) -> list:
+    """The headers of csrc/ and include/ that a source includes, directly or not."""
+    seen = [] if seen is None else seen
+    for name in re.findall(r'#include "([^"]+)"', open(path).read()):
+        for folder in (CSRC, INCLUDE):
+            p = os.path.join(folder, name)
+            if os.path.exists(p) and p not in seen:
+                seen.append(p)
+                _included(p, seen)
+    return seen
+
+
 def build_synth(force: bool = False) -> str:
     src = os.path.join(PKG, "synth", "gen.c")
     if force or _stale(SYNTH_LIB, [src]):
@@ -72,11 +87,13 @@ def build_engine(force: bool = False, verbose: bool = False, extra_flags=()) -> 
     objs = []
     for s in srcs:
         obj = os.path.join(objdir, os.path.basename(s) + ".o")
+        objs.append(obj)
+        if not (force or extra_flags or _stale(obj, [s] + _included(s))):
+            continue
         cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", obj]
         if verbose and s.endswith(".cu"):
             cmd += ["-Xptxas", "-v"]
         subprocess.check_call(cmd)
-        objs.append(obj)
     subprocess.check_call([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs,
                            "-o", ENGINE_LIB, "-lcudart"])
     return ENGINE_LIB

@@ -1,0 +1,35 @@
+// Host-side argument checks shared by the prompt operators (declared in include/tre.h).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <string>
+
+#include "tre_internal.h"
+
+#define TRE_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace tre {
+
+inline tre_status op_error(tre_status st, const char* op, const std::string& what) {
+  set_error(std::string(op) + ": " + what);
+  return st;
+}
+
+inline tre_status op_launch_status(const char* op) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+}
+
+inline bool ptr16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// SMs of the current device (cached per device: the attribute query costs microseconds).
+int device_sms();
+
+// Device address of the status word that tre_ops_status reports (NULL when the module
+// cannot be loaded).
+int32_t* ops_status_ptr();
+
+}  // namespace tre
+
+#define OP_ARG(cond, op, what) \
+  if (!(cond)) return tre::op_error(TRE_ERR_INVALID_ARG, op, what)

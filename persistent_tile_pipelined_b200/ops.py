@@ -1,0 +1,234 @@
+"""The prompt operators on torch tensors (``include/tre.h``, operators of the prompt path).
+
+Each function checks its tensors, allocates what it returns with torch (on the current
+stream, so it may be captured in a CUDA graph), and enqueues the native kernel on torch's
+current stream of the tensors' device.  What a C caller could get wrong too raises
+``tre.TreError``; a tensor of another type, device or shape raises ``ValueError``.  The
+operators have no backward pass: an input that requires a gradient is refused while
+gradients are recorded.
+"""
+from __future__ import annotations
+
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from . import tre
+from .synth import mxfp4_pitch
+
+_TYPES = {torch.bfloat16: tre.TRE_BF16, torch.float32: tre.TRE_F32}
+
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _tensor(t, name: str, ndim: int, dtypes, device=None) -> None:
+    _need(isinstance(t, torch.Tensor), f"{name} must be a tensor")
+    _need(t.ndim == ndim, f"{name} must have {ndim} dimensions, not {t.ndim}")
+    _need(t.dtype in dtypes, f"{name} has type {t.dtype}")
+    _need(t.is_cuda, f"{name} must be on a CUDA device")
+    _need(device is None or t.device == device, f"{name} is on {t.device}, not on {device}")
+    _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1,
+          f"{name}'s last dimension must be contiguous")
+    _need(not (t.requires_grad and torch.is_grad_enabled()),
+          f"{name} requires a gradient: the operator has no backward pass")
+
+
+def _span(t) -> Tuple[int, int]:
+    """The bytes [first, last) that the tensor's elements lie in."""
+    if t.numel() == 0:
+        return 0, 0
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(out, name: str, /, **inputs) -> None:
+    a, b = _span(out)
+    for key, t in inputs.items():
+        if t is not None:
+            c, d = _span(t)
+            _need(b <= c or d <= a, f"{name} may not overlap {key}")
+
+
+def _stream(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _offsets(t, name: str, device) -> None:
+    _tensor(t, name, 1, (torch.int32,), device)
+    _need(t.numel() >= 2, f"{name} must have at least 2 entries")
+
+
+def prompt_attention(q, k, v, q_offsets=None, kv_offsets=None, scale: Optional[float] = None,
+                     out=None):
+    """Causal attention of packed prompts; returns ``out`` [T, Hq, D] bf16.
+
+    q [T, Hq, D], k and v [Hkv, S, D] bf16 in any strides of whole 16-byte units whose last
+    dimension is contiguous: an engine's cache ``k_cache[:, :pos + T]`` as it is, packed rows
+    [S, Hkv, D] as ``k.transpose(0, 1)``.  D is 64 or 128 and Hq a multiple of Hkv.
+    q_offsets, kv_offsets: int32 [n + 1] on the device, the rows of each of n sequences (read
+    when the kernel runs); both None: one sequence.  The last query row of a sequence sees
+    its last key row; a row that sees no key is zero; rows of no sequence are left as they
+    are in ``out`` (unwritten in an ``out`` that the call allocates).
+    scale: 1 / sqrt(D) when None."""
+    _tensor(q, "q", 3, (torch.bfloat16,))
+    _tensor(k, "k", 3, (torch.bfloat16,), q.device)
+    _tensor(v, "v", 3, (torch.bfloat16,), q.device)
+    T, Hq, D = q.shape
+    Hkv, S, _ = k.shape
+    _need(k.shape == v.shape and k.shape[2] == D,
+          f"shapes do not fit: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    _need((q_offsets is None) == (kv_offsets is None), "q_offsets and kv_offsets go together")
+    n = 0
+    if q_offsets is not None:
+        _offsets(q_offsets, "q_offsets", q.device)
+        _offsets(kv_offsets, "kv_offsets", q.device)
+        _need(q_offsets.numel() == kv_offsets.numel(), "q_offsets and kv_offsets differ in length")
+        n = q_offsets.numel() - 1
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _tensor(out, "out", 3, (torch.bfloat16,), q.device)
+        _need(out.shape == q.shape, f"out has shape {tuple(out.shape)}")
+        _need(T <= 1 or out.stride(0) >= D and (Hq <= 1 or out.stride(1) >= D), "out overlaps itself")
+        _apart(out, "out", q=q, k=k, v=v)
+    a = tre.tre_attention(Hq, Hkv, D, n, T, S, q.stride(0), q.stride(1), k.stride(1), k.stride(0),
+                          v.stride(1), v.stride(0), out.stride(0), out.stride(1),
+                          1.0 / math.sqrt(D) if scale is None else scale)
+    sms = torch.cuda.get_device_properties(q.device).multi_processor_count
+    need = tre.tre_prompt_attention_workspace(a, sms)
+    with torch.cuda.device(q.device):
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        tre.check(tre.tre_prompt_attention(
+            a, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr() if n else 0,
+            kv_offsets.data_ptr() if n else 0, out.data_ptr(), ws.data_ptr() if need else 0, need,
+            _stream(q.device)), "tre_prompt_attention")
+    return out
+
+
+def mxfp4_quantize(w, out=None):
+    """Weights [..., K] (bf16 or fp32, K a multiple of 32) to the engine's MXFP4 rows, uint8
+    [..., mxfp4_pitch(K)]: per 32 weights the scale 2^(floor(log2(max)) - 2), codes to the
+    nearest (ties to even), larger magnitudes saturated; a group with a NaN or an infinity
+    stands for NaN."""
+    _need(isinstance(w, torch.Tensor) and w.ndim >= 1, "w must be a tensor of at least one row")
+    flat = w.reshape(-1, w.shape[-1]) if w.numel() else w.new_empty((0, w.shape[-1]))
+    _tensor(flat, "w", 2, tuple(_TYPES))
+    R, K = flat.shape
+    _need(K > 0 and K % 32 == 0, f"rows must have a positive multiple of 32 weights, not {K}")
+    shape = (*w.shape[:-1], mxfp4_pitch(K))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8, device=w.device)
+    else:
+        _tensor(out, "out", len(shape), (torch.uint8,), w.device)
+        _need(tuple(out.shape) == shape and out.is_contiguous(),
+              f"out must be contiguous and of shape {shape}")
+        _apart(out, "out", w=flat)
+    with torch.cuda.device(w.device):
+        tre.check(tre.tre_mxfp4_quantize(flat.data_ptr(), _TYPES[w.dtype], R, K, flat.stride(0),
+                                         out.data_ptr(), _stream(w.device)),
+                  "tre_mxfp4_quantize")
+    return out
+
+
+def _rows(w, name: str, ndim: Optional[int], K: int) -> None:
+    _tensor(w, name, w.ndim if ndim is None and isinstance(w, torch.Tensor) else ndim or 1,
+            (torch.uint8,))
+    _need(K > 0 and K % 32 == 0, f"k must be a positive multiple of 32, not {K}")
+    _need(w.shape[-1] == mxfp4_pitch(K),
+          f"{name}'s rows of {K} weights have {mxfp4_pitch(K)} bytes, not {w.shape[-1]}")
+    _need(w.is_contiguous(), f"{name} must be contiguous")
+
+
+def mxfp4_dequantize(w, k: int, out_dtype=torch.bfloat16, out=None):
+    """The numbers that MXFP4 rows [..., mxfp4_pitch(k)] stand for, [..., k] in bf16 or fp32
+    (exact in both)."""
+    _rows(w, "w", None, k)
+    _need(out_dtype in _TYPES, f"out_dtype {out_dtype} is not bf16 or fp32")
+    shape = (*w.shape[:-1], k)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=w.device)
+    else:
+        _tensor(out, "out", len(shape), (out_dtype,), w.device)
+        _need(tuple(out.shape) == shape and out.is_contiguous(),
+              f"out must be contiguous and of shape {shape}")
+        _apart(out, "out", w=w)
+    with torch.cuda.device(w.device):
+        tre.check(tre.tre_mxfp4_dequantize(w.data_ptr(), w.numel() // w.shape[-1], k,
+                                           _TYPES[out_dtype], out.data_ptr(), _stream(w.device)),
+                  "tre_mxfp4_dequantize")
+    return out
+
+
+def mxfp4_matmul(x, w, offsets=None, out_dtype=torch.float32, out=None):
+    """y[t] = W_e x[t] for the rows t in [offsets[e], offsets[e + 1]); returns [T, N].
+
+    x [T, K] bf16 (row stride of whole 16-byte units), w [E, N, mxfp4_pitch(K)] uint8 (an
+    expert slot of ``upload_moe_model`` as it is) or [N, mxfp4_pitch(K)], offsets int32
+    [E + 1] on the device (read when the kernel runs) or None with one expert: every row.
+    Rows of no expert are left as they are in ``out`` (unwritten in an ``out`` that the call
+    allocates)."""
+    _tensor(x, "x", 2, (torch.bfloat16,))
+    T, K = x.shape
+    if isinstance(w, torch.Tensor) and w.ndim == 2:
+        w = w.unsqueeze(0)
+    _rows(w, "w", 3, K)
+    _need(w.device == x.device, f"w is on {w.device}, not on {x.device}")
+    E, N, _ = w.shape
+    _need(E >= 1 and N >= 1, f"w has shape {tuple(w.shape)}")
+    _need(out_dtype in _TYPES, f"out_dtype {out_dtype} is not bf16 or fp32")
+    _need(offsets is not None or E == 1, "several experts need offsets")
+    if offsets is not None:
+        _offsets(offsets, "offsets", x.device)
+        _need(offsets.numel() == E + 1, f"offsets must have {E + 1} entries")
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+    else:
+        _tensor(out, "out", 2, (out_dtype,), x.device)
+        _need(tuple(out.shape) == (T, N), f"out has shape {tuple(out.shape)}")
+        _apart(out, "out", x=x, w=w, offsets=offsets)
+    with torch.cuda.device(x.device):
+        tre.check(tre.tre_mxfp4_matmul(
+            x.data_ptr(), x.stride(0), w.data_ptr(), offsets.data_ptr() if offsets is not None
+            else 0, E, T, N, K, _TYPES[out_dtype], out.data_ptr(), out.stride(0),
+            _stream(x.device)), "tre_mxfp4_matmul")
+    return out
+
+
+def add_rmsnorm(x, delta, gain, eps: float, x_out=None, out=None):
+    """(x + delta, bf16((x + delta) * gain / sqrt(mean((x + delta)^2) + eps))).
+
+    x [T, d] fp32, delta [T, d] bf16 or fp32 or None, gain [d] bf16, d a multiple of 8.
+    x_out may be x: the residual stream updated in place."""
+    _tensor(x, "x", 2, (torch.float32,))
+    T, d = x.shape
+    if delta is not None:
+        _tensor(delta, "delta", 2, tuple(_TYPES), x.device)
+        _need(delta.shape == x.shape, f"delta has shape {tuple(delta.shape)}")
+    _tensor(gain, "gain", 1, (torch.bfloat16,), x.device)
+    _need(gain.shape[0] == d, f"gain has {gain.shape[0]} entries, not {d}")
+    if x_out is None:
+        x_out = torch.empty((T, d), dtype=torch.float32, device=x.device)
+    elif x_out is not x:
+        _tensor(x_out, "x_out", 2, (torch.float32,), x.device)
+        _need(x_out.shape == x.shape, f"x_out has shape {tuple(x_out.shape)}")
+        if x_out.data_ptr() != x.data_ptr() or x_out.stride() != x.stride():
+            _apart(x_out, "x_out", x=x)
+    if out is None:
+        out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+    else:
+        _tensor(out, "out", 2, (torch.bfloat16,), x.device)
+        _need(out.shape == x.shape, f"out has shape {tuple(out.shape)}")
+    _apart(x_out, "x_out", delta=delta, gain=gain, out=out)
+    _apart(out, "out", x=x, delta=delta, gain=gain)
+    with torch.cuda.device(x.device):
+        tre.check(tre.tre_add_rmsnorm(
+            x.data_ptr(), x.stride(0), delta.data_ptr() if delta is not None else 0,
+            _TYPES[delta.dtype] if delta is not None else 0,
+            delta.stride(0) if delta is not None else 0, gain.data_ptr(), eps, T, d,
+            x_out.data_ptr(), x_out.stride(0), out.data_ptr(), out.stride(0), _stream(x.device)),
+            "tre_add_rmsnorm")
+    return x_out, out

@@ -29,6 +29,7 @@ TRE_LAYER_GQA, TRE_LAYER_MLA, TRE_LAYER_MOE = 0, 1, 2
 TRE_WEIGHTS_BF16, TRE_WEIGHTS_FP8_BLOCK128, TRE_WEIGHTS_FP4_EXPERTS = 0, 1, 2
 TRE_DEBUG_HIDDEN, TRE_DEBUG_TRACE, TRE_DEBUG_FAULT_INJECT, TRE_DEBUG_NO_OVERLAP = 1, 2, 4, 8
 TRE_W_SLOTS = 16
+TRE_BF16, TRE_F32 = 0, 1
 TRACE_COLS = 8
 GQA_SLOTS = {"attn_norm": 0, "wq": 1, "wk": 2, "wv": 3, "wo": 4, "ffn_norm": 5, "wgate": 6,
              "wup": 7, "wdown": 8}
@@ -70,6 +71,14 @@ class tre_plan_info(ctypes.Structure):
                                       "min_sm_bytes")]
 
 
+class tre_attention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_q_heads", "n_kv_heads", "head_dim", "n_seqs", "n_q_rows", "n_kv_rows")] + [
+        (n, ctypes.c_int64) for n in (
+            "q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride", "v_row_stride",
+            "v_head_stride", "out_row_stride", "out_head_stride")] + [("scale", ctypes.c_float)]
+
+
 TRE_LAUNCH_PERSISTENT, TRE_LAUNCH_PER_OP = 0, 1
 
 EXPORTED = ("tre_create", "tre_destroy", "tre_decode_step", "tre_decode_step_host",
@@ -77,7 +86,9 @@ EXPORTED = ("tre_create", "tre_destroy", "tre_decode_step", "tre_decode_step_hos
             "tre_debug_check",
             "tre_decode_tokens", "tre_decode_loop", "tre_set_launch_mode", "tre_get_status",
             "tre_reset", "tre_debug_hidden", "tre_debug_trace", "tre_step_bytes",
-            "tre_plan_inspect", "tre_plan_tasks", "tre_plan_op_groups", "tre_last_error")
+            "tre_plan_inspect", "tre_plan_tasks", "tre_plan_op_groups", "tre_last_error",
+            "tre_prompt_attention", "tre_prompt_attention_workspace", "tre_mxfp4_quantize",
+            "tre_mxfp4_dequantize", "tre_mxfp4_matmul", "tre_add_rmsnorm", "tre_ops_status")
 
 
 def _load() -> ctypes.CDLL:
@@ -112,13 +123,25 @@ def _load() -> ctypes.CDLL:
                                    ctypes.POINTER(tre_plan_info)]
     L.tre_plan_tasks.argtypes = [ctypes.POINTER(tre_config), i32, i32, vp, i32, vp]
     L.tre_plan_tasks.restype = i32
+    f32, sz = ctypes.c_float, ctypes.c_size_t
+    L.tre_prompt_attention_workspace.argtypes = [ctypes.POINTER(tre_attention), i32,
+                                                 ctypes.POINTER(sz)]
+    L.tre_prompt_attention.argtypes = [ctypes.POINTER(tre_attention), vp, vp, vp, vp, vp, vp, vp,
+                                       sz, vp]
+    L.tre_mxfp4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp]
+    L.tre_mxfp4_dequantize.argtypes = [vp, i64, i64, i32, vp, vp]
+    L.tre_mxfp4_matmul.argtypes = [vp, i64, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp]
+    L.tre_add_rmsnorm.argtypes = [vp, i64, vp, i32, i64, vp, f32, i64, i64, vp, i64, vp, i64, vp]
+    L.tre_ops_status.argtypes = [ctypes.POINTER(i32)]
     L.tre_last_error.argtypes = []
     L.tre_last_error.restype = ctypes.c_char_p
     for name in ("tre_create", "tre_decode_step", "tre_decode_step_host",
                  "tre_decode_step_static", "tre_layers_step", "tre_debug_routing",
                  "tre_debug_index", "tre_debug_check", "tre_decode_tokens", "tre_decode_loop", "tre_set_launch_mode", "tre_get_status",
                  "tre_reset", "tre_debug_hidden", "tre_debug_trace", "tre_step_bytes",
-                 "tre_plan_inspect"):
+                 "tre_plan_inspect", "tre_prompt_attention", "tre_prompt_attention_workspace",
+                 "tre_mxfp4_quantize", "tre_mxfp4_dequantize", "tre_mxfp4_matmul",
+                 "tre_add_rmsnorm", "tre_ops_status"):
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -127,9 +150,10 @@ lib = _load()
 
 
 class TreError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, msg: Optional[str] = None):
         self.status = status
-        msg = lib.tre_last_error().decode(errors="replace")
+        if msg is None:
+            msg = lib.tre_last_error().decode(errors="replace")
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
 
 
@@ -286,6 +310,56 @@ def tre_plan_tasks(cfg: tre_config, num_sms: int = 148, smem_per_block: int = 23
     return tasks, begin
 
 
+def tre_prompt_attention_workspace(a: tre_attention, num_sms: int = 148) -> int:
+    b = ctypes.c_size_t()
+    check(lib.tre_prompt_attention_workspace(ctypes.byref(a), int(num_sms), ctypes.byref(b)),
+          "tre_prompt_attention_workspace")
+    return b.value
+
+
+def tre_prompt_attention(a: tre_attention, q: int, k: int, v: int, q_offsets: int,
+                         kv_offsets: int, out: int, workspace: int = 0, workspace_bytes: int = 0,
+                         stream: int = 0) -> int:
+    return lib.tre_prompt_attention(ctypes.byref(a), q or None, k or None, v or None,
+                                    q_offsets or None, kv_offsets or None, out or None,
+                                    workspace or None, int(workspace_bytes), stream or None)
+
+
+def tre_mxfp4_quantize(w: int, dtype: int, rows: int, k: int, w_row_stride: int, out: int,
+                       stream: int = 0) -> int:
+    return lib.tre_mxfp4_quantize(w or None, dtype, rows, k, w_row_stride, out or None,
+                                  stream or None)
+
+
+def tre_mxfp4_dequantize(w: int, rows: int, k: int, dtype: int, out: int, stream: int = 0) -> int:
+    return lib.tre_mxfp4_dequantize(w or None, rows, k, dtype, out or None, stream or None)
+
+
+def tre_mxfp4_matmul(x: int, x_row_stride: int, w: int, offsets: int, n_experts: int, rows: int,
+                     n: int, k: int, out_type: int, out: int, out_row_stride: int,
+                     stream: int = 0) -> int:
+    return lib.tre_mxfp4_matmul(x or None, x_row_stride, w or None, offsets or None, n_experts,
+                                rows, n, k, out_type, out or None, out_row_stride,
+                                stream or None)
+
+
+def tre_add_rmsnorm(x: int, x_row_stride: int, delta: int, delta_type: int,
+                    delta_row_stride: int, gain: int, eps: float, rows: int, d: int, x_out: int,
+                    x_out_row_stride: int, out: int, out_row_stride: int,
+                    stream: int = 0) -> int:
+    return lib.tre_add_rmsnorm(x or None, x_row_stride, delta or None, delta_type,
+                               delta_row_stride, gain or None, float(eps), rows, d,
+                               x_out or None, x_out_row_stride, out or None, out_row_stride,
+                               stream or None)
+
+
+def tre_ops_status() -> int:
+    """Wait for the current device, then the prompt operators' device status (cleared)."""
+    st = ctypes.c_int32()
+    check(lib.tre_ops_status(ctypes.byref(st)), "tre_ops_status")
+    return st.value
+
+
 # ---- convenience ------------------------------------------------------------------------------
 def config_from_workload(wl, **overrides) -> tre_config:
     c = tre_config()
@@ -334,8 +408,10 @@ def upload_moe_model(wl, model: dict, device="cuda:0", expert_fn=None) -> dict:
     routed experts of every layer stacked expert-major into slots 10-12 ([E][Fe][d] gate
     and up, [E][d][Fe] down; FP4 workloads: MXFP4 row bytes [E][Fe][pitch(d)] and
     [E][d][pitch(Fe)]).  `expert_fn(layer, e)` returns an expert's host tensors (default: the
-    workload's generator, one expert at a time)."""
+    workload's generator, one expert at a time).  For FP4 workloads a matrix of `expert_fn`
+    may also be bf16 words [rows][k]: it is quantised on the device (ops.mxfp4_quantize)."""
     import torch
+    from . import ops
     from .synth import mxfp4_pitch
     from .synth import workloads as W
     expert_fn = expert_fn or (lambda l, e: W.gen_expert(wl, l, e))
@@ -356,7 +432,11 @@ def upload_moe_model(wl, model: dict, device="cuda:0", expert_fn=None) -> dict:
         for e in range(E):
             eg, eu, ed = expert_fn(l, e)
             if fp4:
-                for dst, a in ((g[e], eg), (u[e], eu), (dn[e], ed)):
+                for dst, a, k in ((g[e], eg, d), (u[e], eu, d), (dn[e], ed, Fe)):
+                    if a.dtype == np.uint16:
+                        assert tuple(a.shape) == (dst.shape[0], k)
+                        ops.mxfp4_quantize(_dev_tensor(a, device), out=dst)
+                        continue
                     assert a.dtype == np.uint8 and tuple(a.shape) == tuple(dst.shape)
                     dst.copy_(torch.from_numpy(a))
                 continue
@@ -470,6 +550,18 @@ class Engine:
         s = stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
         check(tre_decode_loop(self.h, token, pos, n_steps, s, tokens_out.data_ptr(),
                               logits.data_ptr() if logits is not None else 0), "tre_decode_loop")
+
+    def prefill(self, tokens, pos: int = 0, x_out=None) -> None:
+        """Run the prompt `tokens` (a list, or an int tensor) at positions pos .. pos + T - 1
+        through the stack with the prompt operators, so that the caches hold [0, pos + T);
+        see prefill.py.  A prompt's first logits come from a step of its last token."""
+        from . import prefill
+        prefill.prefill(self, tokens, pos, x_out)
+
+    def prefill_layers(self, x_in, pos: int = 0, x_out=None):
+        """The same for a layers-only stack: x_out [T][d] = stack(x_in [T][d]) (fp32)."""
+        from . import prefill
+        return prefill.prefill_layers(self, x_in, pos, x_out)
 
     def set_launch_mode(self, mode: int) -> int:
         """TRE_LAUNCH_PERSISTENT or TRE_LAUNCH_PER_OP; returns launches per step."""
