@@ -25,7 +25,7 @@ SYNTH_LIB = os.path.join(PKG, "synth", "libtre_synth.so")
 
 ENGINE_SOURCES = ["planner.cpp", "tre_api.cu", "engine.cu", "noalloc.cu",
                   "prompt_attention.cu", "mxfp4.cu", "mxfp4_matmul.cu", "add_rmsnorm.cu",
-                  "ops_status.cu"]
+                  "ops_host.cu"]
 
 
 def engine_headers():

@@ -1,72 +1,379 @@
 // Rows of activations times MXFP4 matrices, grouped by expert (declared in include/tre.h as
 // tre_mxfp4_matmul).
+//
+// out^T = W x^T on the tensor cores: 128 matrix rows are the M side, kN rows of x the N side.
+// An E2M1 number times a power of two has two significant bits, so the decoded weight is
+// exact in bf16 and the product is kind::f16 with fp32 sums; the activations keep their
+// bits.  Per stage of kKS weights the copy warp brings the codes of 128 rows and the kN rows
+// of x into shared memory; two warpgroups take stages in turn, one thread per matrix row,
+// and write the decoded weights straight into tensor memory, where the product reads its A
+// side (no second trip through shared memory, no swizzle, no proxy fence); one thread issues
+// the products.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp4.h>
 
 #include <algorithm>
 
-#include "ops_host.h"
+#include "tc.cuh"
+#include "tensor_map.h"
 
 namespace tre {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kTok = 4;  // rows of x per pass over a matrix row
+constexpr int kRows = 128;          // matrix rows per CTA
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kThreadsMm = 320;  // warps 0-7: two decode warpgroups
 
-// One warp per matrix row: lane l takes the groups of 8 weights l, l + 32, ... against
-// kTok rows of x at a time.
+template <int N>
+struct Tile {
+  static constexpr int KS = N >= 128 ? 64 : 128;     // weights per stage
+  static constexpr int ST = N == 256 ? 6 : N == 128 ? 5 : N == 64 ? 4 : N == 32 ? 6 : 8;
+  static constexpr int kABufs = N == 256 ? 8 : N == 128 ? 4 : 3;
+  static constexpr int kACols = KS / 2;              // tensor-memory columns of one A stage
+  static constexpr int kCols = N == 256 ? 512 : 256;
+  static constexpr int kDCol = kABufs * kACols;
+  static constexpr int kXBytes = N * KS * 2, kWBytes = kRows * KS / 2;
+  static constexpr int kStage = kXBytes + kWBytes;
+  static constexpr int kSmem = ST * kStage + 1024 + 256;
+  static constexpr int kCtas = N == 256 ? 1 : 2;     // per SM
+  static_assert(kDCol + N <= kCols, "tensor memory");
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
+};
+
+struct MatmulParams {
+  const uint8_t* w;
+  const int32_t* offsets;
+  void* out;
+  int64_t out_stride, pitch;
+  int32_t rows, n, k, n_experts, splits;
+  int32_t* status;
+};
+
+// The bf16 pairs of 8 codes (a little-endian word: element 2i in the low nibble of byte i),
+// unscaled: the code's exponent and mantissa bits sit in bf16's lowest exponent and highest
+// mantissa bits, which is the number times 2^-126 (its subnormal 0.5 included).  Both bytes
+// of each half come from whole-word shifts and masks, then byte permutes pair them.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t* o) {
+  const uint32_t he = ((w << 4) & 0x80808080u) | ((w >> 2) & 0x01010101u);  // even, high bytes
+  const uint32_t le = (w << 6) & 0xc0c0c0c0u;
+  const uint32_t ho = (w & 0x80808080u) | ((w >> 6) & 0x01010101u);
+  const uint32_t lo = (w << 2) & 0xc0c0c0c0u;
+  const uint32_t e01 = __byte_perm(le, he, 0x5140), e23 = __byte_perm(le, he, 0x7362);
+  const uint32_t o01 = __byte_perm(lo, ho, 0x5140), o23 = __byte_perm(lo, ho, 0x7362);
+  o[0] = __byte_perm(e01, o01, 0x5410);
+  o[1] = __byte_perm(e01, o01, 0x7632);
+  o[2] = __byte_perm(e23, o23, 0x5410);
+  o[3] = __byte_perm(e23, o23, 0x7632);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 32 codes times their scale 2^(s - 127) as 16 bf16 pairs.  The pattern's 2^-126 and the
+// scale make one exact factor 2^(s - 1), representable up to s = 128; larger scales (and NaN,
+// 255) multiply once more.
+__device__ __forceinline__ void decode32(const uint4 c, uint32_t s, uint32_t* o) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  const uint32_t f = (min(s, 128u) + 126u) << 7;
+  const uint32_t f2 = f | f << 16;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e2m1x8(w[j], o + 4 * j);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = mul_bf16x2(o[j], f2);
+  if (s > 128u) {
+    const uint32_t h = s == 255u ? 0x7fc0u : (s - 1u) << 7;
+    const uint32_t h2 = h | h << 16;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = mul_bf16x2(o[j], h2);
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t smem_addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
 template <class Out>
-__global__ void __launch_bounds__(kWarps * 32)
-    mxfp4_matmul_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride,
-                        const uint8_t* __restrict__ w, const int32_t* __restrict__ offsets,
-                        int rows, int64_t n, int64_t k, int64_t pitch, Out* __restrict__ out,
-                        int64_t out_stride) {
-  const int e = blockIdx.y;
-  const int lo = offsets ? min(max(offsets[e], 0), rows) : 0;
-  const int hi = offsets ? min(max(offsets[e + 1], 0), rows) : rows;
-  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (r >= n) return;
-  const int lane = threadIdx.x & 31;
-  const uint8_t* wr = w + ((int64_t)e * n + r) * pitch;
-  for (int t0 = lo; t0 < hi; t0 += kTok) {
-    float acc[kTok] = {};
-    for (int64_t g = lane; g < k / 8; g += 32) {
-      const uint32_t codes = *reinterpret_cast<const uint32_t*>(wr + g * 4);
-      const uint32_t s = wr[k / 2 + g / 4];
-      const float scale =
-          __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7fc00000u : s << 23);
-      float v[8];
+__device__ __forceinline__ void put(Out* p, float v) {
+  if constexpr (sizeof(Out) == 4) *p = v;
+  else *p = __float2bfloat16_rn(v);
+}
+
+template <int N, class Out>
+__global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
+    mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap xmap,
+                        const __grid_constant__ CUtensorMap wmap, const MatmulParams p) {
+  using T = Tile<N>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + T::ST * T::kStage);
+  uint64_t* empty = full + T::ST;
+  uint64_t* a_full = empty + T::ST;
+  uint64_t* a_empty = a_full + T::kABufs;
+  uint64_t* done = a_empty + T::kABufs;
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up, tile[3];  // expert, first row of x, rows of x
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // the tile's expert: tiles of kN rows, expert by expert
+  if (warp == 0) {
+    int y = blockIdx.y, found = -1, row = 0, count = 0;
+    if (!p.offsets) {
+      found = 0;
+      row = y * N;
+      count = p.rows - row;
+    } else {
+      for (int e0 = 0; e0 < p.n_experts && found < 0; e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < p.n_experts) {
+          lo = min(max(p.offsets[e], 0), p.rows);
+          hi = min(max(p.offsets[e + 1], 0), p.rows);
+        }
+        const int tiles = hi > lo ? (hi - lo + N - 1) / N : 0;
+        int sum = tiles;  // inclusive over the lanes
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(
-            (__nv_fp4x2_storage_t)(codes >> (8 * j) & 0xffu), __NV_E2M1);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        v[2 * j] = f.x * scale;
-        v[2 * j + 1] = f.y * scale;
-      }
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (t0 + i >= hi) continue;
-        const uint4 q = *reinterpret_cast<const uint4*>(x + (int64_t)(t0 + i) * x_stride + g * 8);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i] = fmaf(v[2 * j], __uint_as_float(u[j] << 16), acc[i]);
-          acc[i] = fmaf(v[2 * j + 1], __uint_as_float(u[j] & 0xffff0000u), acc[i]);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += up;
+        }
+        const uint32_t mine = __ballot_sync(0xffffffffu, sum > y);
+        if (mine) {
+          const int l = __ffs(mine) - 1;
+          const int before = __shfl_sync(0xffffffffu, sum - tiles, l);
+          found = e0 + l;
+          row = __shfl_sync(0xffffffffu, lo, l) + (y - before) * N;
+          count = __shfl_sync(0xffffffffu, hi, l) - row;
+        } else {
+          y -= __shfl_sync(0xffffffffu, sum, 31);
         }
       }
     }
+    if (lane == 0) {
+      tile[0] = found;
+      tile[1] = row;
+      tile[2] = min(count, N);
+      gave_up = 0;
+    }
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < T::ST; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < T::kABufs; ++i) {
+      mbar_init(a_full + i, 4);
+      mbar_init(a_empty + i, 1);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int expert = tile[0], t0 = tile[1], nt = tile[2];
+  if (expert < 0) return;  // the same for every CTA of the cluster
+  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, T::kCols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+
+  const int split = p.splits > 1 ? (int)cluster_rank() : 0;
+  const int r0 = (int)(blockIdx.x / p.splits) * kRows;
+  const int all = (p.k + T::KS - 1) / T::KS;
+  const int s0 = (int)((int64_t)all * split / p.splits);
+  const int stages = (int)((int64_t)all * (split + 1) / p.splits) - s0;
+
+  if (warp == kCopyWarp) {
+    if (tc::elect_one()) {
+      int it = 0;
+      for (; it < stages; ++it) {
+        const int slot = it % T::ST;
+        if (!tc::wait(empty + slot, (it / T::ST & 1) ^ 1, &gave_up)) break;
+        uint8_t* x = ring + slot * T::kStage;
+        const int k0 = (s0 + it) * T::KS;
+        mbar_arrive_expect_tx(full + slot, T::kStage);
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
+        for (int h = 0; h < T::KS / 64; ++h)
+          tc::load_2d(x + h * N * 128, &xmap, k0 + h * 64, t0, full + slot);
+        tc::load_2d(x + T::kXBytes, &wmap, k0 / 2, expert * p.n + r0, full + slot);
+      }
+      if (gave_up)  // copies in flight land before the CTA ends
+        for (int i = max(0, it - T::ST); i < it; ++i)
+          for (int n = 0; n < 100000 && !mbar_try_wait(full + i % T::ST, i / T::ST & 1); ++n) {
+          }
+    }
+  } else if (warp == kMmaWarp) {
+    if (tc::elect_one()) {
+      constexpr uint32_t idesc = tc::idesc_bf16(kRows, N, 0);
+      bool ok = true;
+      for (int it = 0; it < stages && ok; ++it) {
+        const int slot = it % T::ST, buf = it % T::kABufs;
+        ok = tc::wait(full + slot, it / T::ST & 1, &gave_up) &&
+             tc::wait(a_full + buf, it / T::kABufs & 1, &gave_up);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t x = smem_u32(ring + slot * T::kStage);
 #pragma unroll
-      for (int sft = 16; sft; sft >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], sft);
-      if (lane == 0 && t0 + i < hi) {
-        if constexpr (sizeof(Out) == 4) out[(int64_t)(t0 + i) * out_stride + r] = acc[i];
-        else out[(int64_t)(t0 + i) * out_stride + r] = __float2bfloat16_rn(acc[i]);
+        for (int j = 0; j < T::KS / 16; ++j) {
+          const uint64_t b = tc::smem_desc(x + (j / 4) * N * 128 + (j % 4) * 32, 16, 1024);
+          tc::mma_ts(tmem + T::kDCol, tmem + buf * T::kACols + j * 8, b, idesc, it + j > 0);
+        }
+        tc::commit(empty + slot);
+        tc::commit(a_empty + buf);
+      }
+      tc::commit(done);
+      if (!ok)
+        for (int n = 0; n < 100000 && !mbar_try_wait(done, 0); ++n) {
+        }
+    }
+  } else {
+    // decode: thread = matrix row r0 + 32 (warp mod 4) + lane, warpgroup = stage parity
+    const int wg = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const int64_t row = (int64_t)expert * p.n + min(r0 + r, p.n - 1);
+    const uint8_t* scales = p.w + row * p.pitch + p.k / 2;
+    const int blocks = p.k / 32;
+    constexpr int kPer = 512 / T::KS;  // stages per 16 scale bytes
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    int group = -1;
+    uint4 sc = make_uint4(0, 0, 0, 0), next = sc;
+    auto fetch = [&](int g) {  // 16 scales; those behind the row's last are never used
+      return g * 16 < blocks ? *reinterpret_cast<const uint4*>(scales + g * 16)
+                             : make_uint4(0, 0, 0, 0);
+    };
+    if (stages > 0) next = fetch(s0 / kPer);
+    for (int it = wg; it < stages; it += 2) {
+      const int st = s0 + it;
+      if (st / kPer != group) {
+        // (a warpgroup never skips a group: a group has at least 4 stages)
+        if (group < 0 && st / kPer != s0 / kPer) next = fetch(st / kPer);
+        group = st / kPer;
+        sc = next;
+        next = fetch(group + 1);
+      }
+      const int slot = it % T::ST, buf = it % T::kABufs;
+      if (!tc::wait_warp(full + slot, it / T::ST & 1, &gave_up)) break;
+      const uint8_t* codes = ring + slot * T::kStage + T::kXBytes + r * (T::KS / 2);
+      const int first = (st % kPer) * (T::KS / 32);  // of the group's 16 scales
+      const uint32_t word = first / 4 == 0 ? sc.x : first / 4 == 1 ? sc.y : first / 4 == 2 ? sc.z : sc.w;
+      uint32_t v[T::KS / 2];
+#pragma unroll
+      for (int c = 0; c < T::KS / 32; ++c) {
+        // 16-byte chunks are swizzled within 128 bytes: by row pair (64-byte rows) or by
+        // groups of four rows (32-byte rows)
+        const int at = T::KS == 128 ? c ^ (r >> 1 & 3) : c ^ (r >> 2 & 1);
+        const uint4 q = *reinterpret_cast<const uint4*>(codes + at * 16);
+        const bool in = st * (T::KS / 32) + c < blocks;  // behind the row's end: zero codes
+        decode32(q, in ? word >> (8 * ((first + c) & 3)) & 0xffu : 0u, v + 16 * c);
+      }
+      if (!tc::wait_warp(a_empty + buf, (it / T::kABufs & 1) ^ 1, &gave_up)) break;
+      tc::fence_after();
+#pragma unroll
+      for (int c = 0; c < T::KS / 64; ++c)
+        tc::tmem_st32(lane_addr + buf * T::kACols + c * 32, v + 32 * c);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full + buf);
+    }
+    __syncwarp();
+    // the sums: warpgroup = half of the rows of x
+    const bool ok = stages == 0 || tc::wait_warp(done, 0, &gave_up);
+    tc::fence_after();
+    Out* out = static_cast<Out*>(p.out);
+    float* part = reinterpret_cast<float*>(ring);  // split along k: [N][128], ring is idle
+    constexpr int kStep = N >= 64 ? 32 : 8;
+    for (int c0 = wg * (N / 2); c0 < min((wg + 1) * (N / 2), nt); c0 += kStep) {
+      uint32_t v[kStep];
+      __syncwarp();
+      if (kStep == 32) tc::tmem_ld32(lane_addr + T::kDCol + c0, v);
+      else tc::tmem_ld8(lane_addr + T::kDCol + c0, v);
+      tc::wait_ld();
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        const float f = stages == 0 ? 0.f : __uint_as_float(v[j]);
+        if (p.splits > 1) {
+          part[(c0 + j) * kRows + r] = f;
+        } else if (ok && c0 + j < nt && r0 + r < p.n) {
+          put(out + (int64_t)(t0 + c0 + j) * p.out_stride + r0 + r, f);
+        }
       }
     }
   }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::fence_after();
+    tc::tmem_free(tmem, T::kCols);
+  }
+  if (p.splits > 1) {
+    // every CTA joins its share of the rows of x, always adding the parts in the same order
+    cluster_sync();
+    const int r = threadIdx.x & (kRows - 1);
+    if (threadIdx.x < 2 * kRows && r0 + r < p.n) {
+      for (int j = split * 2 + (threadIdx.x >> 7); j < nt; j += 2 * p.splits) {
+        float sum = 0.f;
+        for (int s = 0; s < p.splits; ++s)
+          sum += ld_cluster(smem_u32(ring) + (uint32_t)(j * kRows + r) * 4, s);
+        put(static_cast<Out*>(p.out) + (int64_t)(t0 + j) * p.out_stride + r0 + r, sum);
+      }
+    }
+    cluster_sync();
+  }
+  if (threadIdx.x == 0 && gave_up) atomicExch(p.status, TRE_ERR_DEP_TIMEOUT);
+}
+
+template <int N, class Out>
+tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap,
+                  const CUtensorMap& wmap, cudaStream_t stream) {
+  using T = Tile<N>;
+  auto kernel = mxfp4_matmul_kernel<N, Out>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  cudaLaunchConfig_t c = {};
+  const int64_t tiles = p.offsets ? (int64_t)p.rows / N + std::min<int64_t>(p.n_experts, p.rows)
+                                  : ((int64_t)p.rows + N - 1) / N;
+  OP_ARG(tiles <= 65535, op, "too many rows for one call");
+  c.gridDim = dim3((unsigned)((p.n + kRows - 1) / kRows * p.splits), (unsigned)tiles);
+  c.blockDim = dim3(kThreadsMm);
+  c.dynamicSmemBytes = T::kSmem;
+  c.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  c.attrs = &attr;
+  c.numAttrs = p.splits > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&c, kernel, xmap, wmap, p);
+  return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+}
+
+// Rows of x per tile: the least of 16 .. 256 that covers twice an expert's average (most
+// experts' weights pass once), but no more than leaves the device without tiles to fill it.
+int tile_rows(const MatmulParams& p, int sms) {
+  const int64_t avg = ((int64_t)p.rows * (p.n_experts > 1 ? 2 : 1) + p.n_experts - 1) / p.n_experts;
+  int best = 16;
+  while (best < 256 && best < avg) best *= 2;
+  const int64_t row_tiles = (p.n + kRows - 1) / kRows;
+  while (best > 64 && row_tiles * ((p.rows + best - 1) / best) < sms) best /= 2;
+  return best;
 }
 
 }  // namespace
@@ -88,6 +395,7 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
   OP_ARG(k > 0 && k % 32 == 0 && k < ((int64_t)1 << 30), op,
          "k must be a positive multiple of 32");
   if (rows == 0) return TRE_OK;
+  tre_status st;
   OP_ARG(ptr16(x) && ptr16(w) && out && ((uintptr_t)out & (out_type == TRE_BF16 ? 1 : 3)) == 0,
          op, "NULL or misaligned pointer");
   OP_ARG(((uintptr_t)offsets & 3) == 0, op, "misaligned offsets");
@@ -95,14 +403,42 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
          "x rows must not overlap and their stride be whole 16-byte units");
   OP_ARG(rows == 1 || out_row_stride >= n, op, "output rows overlap");
   const int64_t pitch = (k / 2 + k / 32 + 15) / 16 * 16;
-  const dim3 grid((unsigned)((n + kWarps - 1) / kWarps), (unsigned)n_experts);
-  if (out_type == TRE_BF16)
-    mxfp4_matmul_kernel<<<grid, kWarps * 32, 0, (cudaStream_t)stream>>>(
-        static_cast<const __nv_bfloat16*>(x), x_row_stride, static_cast<const uint8_t*>(w),
-        offsets, (int)rows, n, k, pitch, static_cast<__nv_bfloat16*>(out), out_row_stride);
-  else
-    mxfp4_matmul_kernel<<<grid, kWarps * 32, 0, (cudaStream_t)stream>>>(
-        static_cast<const __nv_bfloat16*>(x), x_row_stride, static_cast<const uint8_t*>(w),
-        offsets, (int)rows, n, k, pitch, static_cast<float*>(out), out_row_stride);
-  return op_launch_status(op);
+  const int sms = device_sms();
+  MatmulParams p{static_cast<const uint8_t*>(w), offsets, out, out_row_stride, pitch,
+                 (int32_t)rows, (int32_t)n, (int32_t)k, n_experts, 1, ops_status_ptr()};
+  OP_ARG(p.status, op, "the operators' status word is not available");
+  const int tile = tile_rows(p, sms);
+  const int ks = tile >= 128 ? 64 : 128;
+  if (tile <= 32) {  // few tiles: split k over a cluster until the device is busy
+    const int64_t tiles = (n + kRows - 1) / kRows *
+                          std::max<int64_t>(1, std::min<int64_t>(rows, (rows + tile - 1) / tile));
+    while (p.splits < 8 && tiles * p.splits * 2 <= 2 * sms && k / ks >= 4 * p.splits) p.splits *= 2;
+  }
+  CUtensorMap xmap, wmap;
+  const uint64_t xd[2] = {(uint64_t)k, (uint64_t)rows};
+  const uint64_t xs[1] = {(uint64_t)(rows == 1 ? k : x_row_stride) * 2};
+  const uint32_t xb[2] = {64, (uint32_t)tile};
+  st = encode_map(op, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xs, xb,
+                  CU_TENSOR_MAP_SWIZZLE_128B, &xmap);
+  if (st != TRE_OK) return st;
+  const uint64_t wd[2] = {(uint64_t)k / 2, (uint64_t)n * n_experts};
+  const uint64_t ws[1] = {(uint64_t)pitch};
+  const uint32_t wb[2] = {(uint32_t)ks / 2, kRows};
+  st = encode_map(op, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, wd, ws, wb,
+                  ks == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, &wmap);
+  if (st != TRE_OK) return st;
+#define MM(N)                                                                            \
+  case N:                                                                                \
+    return out_type == TRE_BF16                                                          \
+               ? launch<N, __nv_bfloat16>(op, p, xmap, wmap, (cudaStream_t)stream)       \
+               : launch<N, float>(op, p, xmap, wmap, (cudaStream_t)stream)
+  switch (tile) {
+    MM(16);
+    MM(32);
+    MM(64);
+    MM(128);
+    default:
+      MM(256);
+  }
+#undef MM
 }

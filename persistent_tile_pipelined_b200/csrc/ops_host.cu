@@ -1,0 +1,74 @@
+// What the operators share on the host: the device status word (declared in include/tre.h as
+// tre_ops_status), the device's size and tensor maps.
+#include "tensor_map.h"
+
+namespace tre {
+
+// One word per device: the module's copy on the current one.
+__device__ int32_t g_ops_status;
+
+int32_t* ops_status_ptr() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_ops_status) == cudaSuccess ? static_cast<int32_t*>(p)
+                                                               : nullptr;
+}
+
+int device_sms() {
+  static int sms[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (!sms[dev]) cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+  return sms[dev] > 0 ? sms[dev] : 148;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e =
+        cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q);
+    return reinterpret_cast<EncodeTiledFn>(
+        e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f : nullptr);
+  }();
+  return fn;
+}
+
+tre_status encode_map(const char* op, CUtensorMapDataType type, int rank, const void* base,
+                      const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                      CUtensorMapSwizzle swizzle, CUtensorMap* out) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return op_error(TRE_ERR_CUDA, op, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i], one[i] = 1;
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  const CUresult r = fn(out, type, rank, const_cast<void*>(base), d, st, b, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TRE_OK
+                           : op_error(TRE_ERR_CUDA, op,
+                                      "cuTensorMapEncodeTiled failed (" +
+                                          std::to_string((int)r) + ")");
+}
+
+}  // namespace tre
+
+using namespace tre;
+
+TRE_EXPORT tre_status tre_ops_status(int32_t* device_status) {
+  static const char* op = "tre_ops_status";
+  OP_ARG(device_status, op, "NULL argument");
+  int32_t v = 0;
+  const int32_t zero = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_ops_status, sizeof(v));
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_ops_status, &zero, sizeof(zero));
+  if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  *device_status = v;
+  return TRE_OK;
+}
