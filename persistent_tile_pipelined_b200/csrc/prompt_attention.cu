@@ -1,82 +1,522 @@
 // Causal attention of packed prompts (declared in include/tre.h as tre_prompt_attention).
+//
+// One CTA takes 256 rows of one key/value head's query group: row r of a sequence is query
+// token r / g, head r mod g of the group, so grouped heads share every key and value tile and
+// a single token of a large group still fills matrix rows.  The rows are two tiles of 128,
+// each with its scores S (fp32, tensor memory), its probabilities P (bf16, over the first half
+// of S) and its output sums O (fp32, tensor memory).  Per 128 keys and tile:
+//   S = Q K^T (operands in shared memory);  a warpgroup, one thread per row, takes the row's
+//   maximum, P = 2^(S c - m) and the row's sum;  O += P V (P read from tensor memory).
+// While one tile is in its softmax the matrix unit works on the other.  The running maximum is
+// only raised, and O rescaled, when it grows by more than 2^8: P then stays below 2^8, which
+// costs bf16 P and fp32 sums no precision, and the rescaling all but disappears.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 
-#include "ops_host.h"
+#include "tc.cuh"
+#include "tensor_map.h"
 
 namespace tre {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTile = 128;                     // rows of a tile, keys of a step
+constexpr int kItemRows = 2 * kTile;           // rows per CTA
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kFixWarp = 10, kFixWarps = 2;
+constexpr int kThreadsAttn = 384;
+constexpr float kRaise = 8.f;                  // log2 of how far P may exceed 1
+
+template <int D>
+struct Shape {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int ST = D == 128 ? 5 : 10;  // key and value tiles in flight
+  static constexpr int kSmem = 2 * kTileBytes + ST * kTileBytes + 1024 + 256;
+  static constexpr int kO = 2 * kTile;          // tensor-memory column of the first O
+};
 
 struct AttnParams {
   tre_attention a;
-  const __nv_bfloat16 *q, *k, *v;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16 *k, *v;  // the slow path's view of what the tensor maps describe
   __nv_bfloat16* out;
   const int32_t *q_offsets, *kv_offsets;
+  float* part_o;       // [splits][n_q_rows * Hq][D]
+  float2* part_ml;     // [splits][n_q_rows * Hq]: maximum, sum (sum -1: no key seen)
+  int32_t tiles;       // upper bound of the row tiles of a kv head
+  int32_t splits;
+  float c;             // scale * log2(e)
+  int32_t* status;
 };
 
-// One warp per (query row, head): the keys in order, 32 at a time, one per lane, with the
-// running maximum and sum of the softmax; then the lanes share the width of v.
+// Work of one CTA: rows [row0, row0 + rows) of sequence rows q0 .. (nq tokens), keys k0 ..
+struct Item {
+  int q0, nq, k0, nk, row0, rows;
+};
+
+// The y-th row tile over all sequences (whole warp); rows = 0 when there is none.
+__device__ Item find_item(const AttnParams& p, int g, int y) {
+  const int lane = threadIdx.x & 31;
+  Item it{0, p.a.n_q_rows, 0, p.a.n_kv_rows, 0, 0};
+  if (p.a.n_seqs == 0) {
+    it.row0 = y * kItemRows;
+  } else {
+    bool found = false;
+    for (int i0 = 0; i0 < p.a.n_seqs && !found; i0 += 32) {
+      const int i = i0 + lane;
+      int qa = 0, qb = 0;
+      if (i < p.a.n_seqs) {
+        qa = min(max(p.q_offsets[i], 0), p.a.n_q_rows);
+        qb = min(max(p.q_offsets[i + 1], 0), p.a.n_q_rows);
+      }
+      const int tiles = qb > qa ? (int)(((int64_t)(qb - qa) * g + kItemRows - 1) / kItemRows) : 0;
+      int sum = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      const uint32_t mine = __ballot_sync(0xffffffffu, sum > y);
+      if (mine) {
+        const int l = __ffs(mine) - 1;
+        found = true;
+        it.row0 = (y - __shfl_sync(0xffffffffu, sum - tiles, l)) * kItemRows;
+        it.q0 = __shfl_sync(0xffffffffu, qa, l);
+        it.nq = __shfl_sync(0xffffffffu, qb, l) - it.q0;
+        it.k0 = min(max(p.kv_offsets[i0 + l], 0), p.a.n_kv_rows);
+        it.nk = max(min(max(p.kv_offsets[i0 + l + 1], 0), p.a.n_kv_rows) - it.k0, 0);
+      } else {
+        y -= __shfl_sync(0xffffffffu, sum, 31);
+      }
+    }
+    if (!found) return it;
+  }
+  const int64_t left = (int64_t)it.nq * g - it.row0;
+  it.rows = left > kItemRows ? kItemRows : left > 0 ? (int)left : 0;
+  return it;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Where a row's result goes: the output, or its part [split] when the keys are split.
+struct RowOut {
+  __nv_bfloat16* out;
+  float* o;
+  float2* ml;
+};
+
+__device__ __forceinline__ RowOut row_out(const AttnParams& p, int D, int split, int tok, int h) {
+  const int64_t at = ((int64_t)split * p.a.n_q_rows + tok) * p.a.n_q_heads + h;
+  return {p.out + (int64_t)tok * p.a.out_row_stride + (int64_t)h * p.a.out_head_stride,
+          p.part_o + at * D, p.part_ml + at};
+}
+
+// One row the long way, by one thread: keys [from, to) of the sequence in order.  Taken by
+// every row of a CTA whose partly visible key tiles hold a NaN or an infinity in v: the matrix
+// product would carry 0 x NaN into rows that do not see the key.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) prompt_attention_kernel(const AttnParams p) {
-  __shared__ float qs[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x, h = blockIdx.y * kWarps + warp;
-  if (h >= p.a.n_q_heads) return;
-  int q0 = 0, q1 = p.a.n_q_rows, k0 = 0, k1 = p.a.n_kv_rows;
-  if (p.a.n_seqs) {
-    int i = 0;
-    for (; i < p.a.n_seqs; ++i) {
-      q0 = min(max(p.q_offsets[i], 0), p.a.n_q_rows);
-      q1 = min(max(p.q_offsets[i + 1], 0), p.a.n_q_rows);
-      if (t >= q0 && t < q1) break;
-    }
-    if (i == p.a.n_seqs) return;
-    k0 = min(max(p.kv_offsets[i], 0), p.a.n_kv_rows);
-    k1 = min(max(p.kv_offsets[i + 1], 0), p.a.n_kv_rows);
-  }
-  const int see = k1 - k0 - (q1 - q0) + (t - q0) + 1;  // keys k0 .. k0 + see - 1
+__device__ __noinline__ void slow_row(const AttnParams& p, int split, int tok, int h, int k0,
+                                      int from, int to, int see) {
   const int kh = h / (p.a.n_q_heads / p.a.n_kv_heads);
-  const __nv_bfloat16* q = p.q + t * p.a.q_row_stride + h * p.a.q_head_stride;
-  const __nv_bfloat16* k = p.k + kh * p.a.k_head_stride;
-  const __nv_bfloat16* v = p.v + kh * p.a.v_head_stride;
-  for (int i = lane; i < D; i += 32) qs[warp][i] = __bfloat162float(q[i]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-  for (int s0 = 0; s0 < see; s0 += 32) {
-    float s = -INFINITY;
-    if (s0 + lane < see) {
-      const __nv_bfloat16* kr = k + (int64_t)(k0 + s0 + lane) * p.a.k_row_stride;
-      float dot = 0.f;
-      for (int i = 0; i < D; ++i) dot = fmaf(qs[warp][i], __bfloat162float(kr[i]), dot);
-      s = dot * p.a.scale;
-    }
-    float mn = s;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-    mn = fmaxf(mn, m);
-    const float shift = mn == -INFINITY ? 0.f : mn;
-    const float c = expf(m - shift);
-    const float e = s0 + lane < see ? expf(s - shift) : 0.f;
+  const __nv_bfloat16* q = p.q + (int64_t)tok * p.a.q_row_stride + (int64_t)h * p.a.q_head_stride;
+  float acc[D], m = -INFINITY, l = 0.f;
+  for (int d = 0; d < D; ++d) acc[d] = 0.f;
+  for (int s = from; s < to; ++s) {
+    const __nv_bfloat16* k =
+        p.k + (int64_t)kh * p.a.k_head_stride + (int64_t)(k0 + s) * p.a.k_row_stride;
+    const __nv_bfloat16* v =
+        p.v + (int64_t)kh * p.a.v_head_stride + (int64_t)(k0 + s) * p.a.v_row_stride;
+    float dot = 0.f;
+    for (int d = 0; d < D; ++d) dot = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), dot);
+    const float x = dot * p.c, mn = fmaxf(m, x), sh = mn == -INFINITY ? 0.f : mn;
+    const float old = m == mn ? 1.f : exp2_approx(m - sh), e = exp2_approx(x - sh);
+    for (int d = 0; d < D; ++d) acc[d] = fmaf(e, __bfloat162float(v[d]), acc[d] * old);
+    l = fmaf(l, old, e);
     m = mn;
-    l *= c;
+  }
+  const RowOut r = row_out(p, D, split, tok, h);
+  if (p.splits > 1) {
+    for (int d = 0; d < D; ++d) r.o[d] = acc[d];
+    *r.ml = make_float2(m, to > from ? l : -1.f);
+  } else {
+    for (int d = 0; d < D; ++d) r.out[d] = __float2bfloat16_rn(see > 0 ? acc[d] / l : 0.f);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsAttn, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
+  using T = Shape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~uintptr_t(1023));
+  uint8_t* ring = qs + 2 * T::kTileBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + T::ST * T::kTileBytes);
+  uint64_t* empty = full + T::ST;
+  uint64_t* q_full = empty + T::ST;
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_done = p_full + 2;
+  uint64_t* v_fixed = o_done + 2;
+  uint64_t* v_check = v_fixed + 1;
+  uint64_t* drained = v_check + 1;
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up, poison;
+  __shared__ Item item;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = p.a.n_q_heads / p.a.n_kv_heads;
+  const int kh = blockIdx.x % p.a.n_kv_heads;
+
+  if (warp == 0) {
+    // the last row tiles first: with causal rows they take longest
+    const Item it = find_item(p, g, p.tiles - 1 - (int)(blockIdx.x / p.a.n_kv_heads));
+    if (lane == 0) {
+      item = it;
+      gave_up = 0;
+      poison = 0;
+    }
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < T::ST; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 4);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(o_done + i, 1);
+    }
+    mbar_init(v_fixed, kFixWarps);
+    mbar_init(v_check, 1);
+    mbar_init(drained, 1);
+    fence_mbar_init();
+  } else if (warp == kCopyWarp && lane == 0 && p.a.n_kv_rows > 0) {
+    tc::prefetch_map(&kmap);
+    tc::prefetch_map(&vmap);
+  }
+  __syncthreads();
+  const Item it = item;
+  if (it.rows == 0) return;
+  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+
+  // keys that a row sees: it.nk - it.nq + (row / g) + 1, not below 0
+  auto sees = [&](int row) { return max(it.nk - it.nq + row / g + 1, 0); };
+  const int subs = it.rows > kTile ? 2 : 1;
+  const int least = sees(it.row0);  // of the CTA's rows
+  int n_sub[2];                     // key tiles of each row tile
+  n_sub[0] = (sees(it.row0 + min(it.rows, kTile) - 1) + kTile - 1) / kTile;
+  n_sub[1] = subs == 2 ? (sees(it.row0 + it.rows - 1) + kTile - 1) / kTile : 0;
+  const int n_all = max(n_sub[0], n_sub[1]);
+  const int split = blockIdx.y;
+  const int kb = (int)((int64_t)n_all * split / p.splits);
+  const int ke = (int)((int64_t)n_all * (split + 1) / p.splits);
+  n_sub[0] = min(n_sub[0], ke);
+  n_sub[1] = min(n_sub[1], ke);
+
+  if (warp == kCopyWarp) {
+    if (tc::elect_one()) {
+      int n = 0;
+      const int total = 2 * (ke - kb);
+      for (; n < total; ++n) {
+        const int slot = n % T::ST;
+        if (!tc::wait(empty + slot, (n / T::ST & 1) ^ 1, &gave_up)) break;
+        uint8_t* dst = ring + slot * T::kTileBytes;
+        mbar_arrive_expect_tx(full + slot, T::kTileBytes);
+        const int row = it.k0 + (kb + n / 2) * kTile;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) acc[j] *= c;
-    for (int x = 0; x < 32 && s0 + x < see; ++x) {
-      const float ex = __shfl_sync(0xffffffffu, e, x);
-      l += ex;
-      const __nv_bfloat16* vr = v + (int64_t)(k0 + s0 + x) * p.a.v_row_stride;
+        for (int h = 0; h < D / 64; ++h)
+          tc::load_3d(dst + h * kTile * 128, n & 1 ? &vmap : &kmap, h * 64, row, kh, full + slot);
+      }
+      if (gave_up)  // copies in flight land before the CTA ends
+        for (int i = max(0, n - T::ST); i < n; ++i)
+          for (int x = 0; x < 100000 && !mbar_try_wait(full + i % T::ST, i / T::ST & 1); ++x) {
+          }
+    }
+  } else if (warp == kMmaWarp) {
+    if (tc::elect_one()) {
+      constexpr uint32_t id_s = tc::idesc_bf16(kTile, kTile, 0);
+      constexpr uint32_t id_o = tc::idesc_bf16(kTile, D, 1);
+      bool ok = true;
+      auto tile_wait = [&](int n) {
+        ok = ok && tc::wait(full + n % T::ST, n / T::ST & 1, &gave_up);
+      };
+      auto scores = [&](int sub, int n) {
+        const uint32_t q = smem_u32(qs + sub * T::kTileBytes);
+        const uint32_t k = smem_u32(ring + n % T::ST * T::kTileBytes);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        acc[j] = fmaf(ex, __bfloat162float(vr[lane + 32 * j]), acc[j]);
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t at = (j / 4) * kTile * 128 + (j % 4) * 32;
+          tc::mma_ss(tmem + sub * kTile, tc::smem_desc(q + at, 16, 1024),
+                     tc::smem_desc(k + at, 16, 1024), id_s, j > 0);
+        }
+        tc::commit(s_full + sub);
+      };
+      auto outputs = [&](int sub, int n, bool add) {
+        const uint32_t v = smem_u32(ring + n % T::ST * T::kTileBytes);
+#pragma unroll
+        for (int j = 0; j < kTile / 16; ++j)
+          tc::mma_ts(tmem + T::kO + sub * D, tmem + sub * kTile + j * 8,
+                     tc::smem_desc(v + j * 2048, kTile * 128, 1024), id_o, add || j > 0);
+        tc::commit(o_done + sub);
+      };
+      if (kb < ke) {
+        for (int sub = 0; sub < subs; ++sub)
+          if (kb < n_sub[sub]) ok = ok && tc::wait(q_full + sub, 0, &gave_up);
+        tile_wait(0);
+        if (ok) {
+          tc::fence_after();
+          for (int sub = 0; sub < subs; ++sub)
+            if (kb < n_sub[sub]) scores(sub, 0);
+          tc::commit(empty + 0);
+        }
+      }
+      int fixed = 0;
+      for (int i = kb; i < ke && ok; ++i) {
+        const int nv = 2 * (i - kb) + 1, nk2 = nv + 1;
+        tile_wait(nv);
+        const bool partly = (i + 1) * kTile > least;
+        if (partly && ok) mbar_arrive(v_check);
+        if (i + 1 < ke) tile_wait(nk2);
+        for (int sub = 0; sub < subs && ok; ++sub) {
+          if (i >= n_sub[sub]) continue;
+          ok = tc::wait(p_full + sub, (i - kb) & 1, &gave_up) &&
+               (!partly || tc::wait(v_fixed, fixed & 1, &gave_up));
+          if (!ok) break;
+          tc::fence_after();
+          outputs(sub, nv, i > kb);
+          if (i + 1 < n_sub[sub]) scores(sub, nk2);
+        }
+        if (!ok) break;
+        fixed += partly;
+        tc::commit(empty + nv % T::ST);
+        if (i + 1 < ke) tc::commit(empty + nk2 % T::ST);
+      }
+      if (!ok) {  // products in flight end before the tensor memory is freed
+        tc::commit(drained);
+        for (int x = 0; x < 100000 && !mbar_try_wait(drained, 0); ++x) {
+        }
+      }
+    }
+  } else if (warp >= kFixWarp) {
+    // Key tiles that some row sees only in part: values of keys behind the sequence become
+    // zero (P is zero there, and 0 x NaN is not), others are looked through for NaN and
+    // infinities.
+    int bad = 0, checked = 0;
+    for (int i = max(kb, least / kTile); i < ke; ++i) {
+      // the product's thread says when the tile is there (a wait on the tile's own barrier
+      // could mistake an earlier round of the ring for this one)
+      if (!tc::wait_warp(v_check, checked++ & 1, &gave_up)) break;
+      uint8_t* v = ring + (2 * (i - kb) + 1) % T::ST * T::kTileBytes;
+      for (int j = max(least - i * kTile, 0) + warp - kFixWarp; j < kTile; j += kFixWarps) {
+        if (lane >= D / 8) continue;
+        uint4* at = reinterpret_cast<uint4*>(v + (lane >> 3) * kTile * 128 + j * 128 + (lane & 7) * 16);
+        if (i * kTile + j >= it.nk) {
+          *at = make_uint4(0, 0, 0, 0);
+        } else {
+          const uint4 x = *at;
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_fixed);
+    }
+    if (bad) poison = 1;
+  } else {
+    const int sub = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int row = it.row0 + sub * kTile + r;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_addr = lane_addr + sub * kTile, o_addr = lane_addr + T::kO + sub * D;
+    if (sub < subs && kb < n_sub[sub]) {
+      // this tile's rows of q, 16 bytes a lane, swizzled; rows that do not exist are zero
+      constexpr int kChunks = D / 8;
+      for (int x = r; x < kTile * kChunks; x += kTile) {
+        const int rr = x / kChunks, ch = x % kChunks, gr = sub * kTile + rr;
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (gr < it.rows) {
+          const int tok = it.q0 + (it.row0 + gr) / g, h = kh * g + (it.row0 + gr) % g;
+          val = *reinterpret_cast<const uint4*>(p.q + (int64_t)tok * p.a.q_row_stride +
+                                                (int64_t)h * p.a.q_head_stride + ch * 8);
+        }
+        *reinterpret_cast<uint4*>(qs + sub * T::kTileBytes + (ch >> 3) * kTile * 128 + rr * 128 +
+                                  (((ch & 7) ^ (rr & 7)) * 16)) = val;
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + sub);
+    }
+    const bool mine = sub * kTile + r < it.rows;
+    const int see = mine ? sees(row) : 0;
+    const int sub_least = sees(it.row0 + sub * kTile);
+    const float c = p.c;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = kb; i < n_sub[sub]; ++i) {
+      ok = tc::wait_warp(s_full + sub, (i - kb) & 1, &gave_up);
+      if (!ok) break;
+      tc::fence_after();
+      uint32_t s[kTile];
+#pragma unroll
+      for (int x = 0; x < kTile; x += 32) tc::tmem_ld32(s_addr + x, s + x);
+      tc::wait_ld();
+      if ((i + 1) * kTile > sub_least) {
+        const int lim = see - i * kTile;
+#pragma unroll
+        for (int x = 0; x < kTile; ++x)
+          if (x >= lim) s[x] = 0xff800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < kTile; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+      const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
+      if (__any_sync(0xffffffffu, top > m + kRaise || (i == kb))) {
+        const float f = top == m ? 1.f : exp2_approx(m - top);
+        m = top;
+        l *= f;
+        if (i > kb) {
+          ok = tc::wait_warp(o_done + sub, (i - kb - 1) & 1, &gave_up);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll
+          for (int x = 0; x < D; x += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_addr + x, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            tc::tmem_st32(o_addr + x, o);
+          }
+        }
+      }
+      const float shift = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < kTile; x += 64) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          const float a = exp2_approx(fmaf(__uint_as_float(s[x + 2 * y]), c, -shift));
+          const float b = exp2_approx(fmaf(__uint_as_float(s[x + 2 * y + 1]), c, -shift));
+          sum[y & 1] += a;
+          sum[2 + (y & 1)] += b;
+          pk[y] = pack_bf16(a, b);
+        }
+        tc::tmem_st32(s_addr + x / 2, pk);
+      }
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + sub);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+    // the row's m and l stay in registers for the end
+    const int n = n_sub[sub] - kb;
+    if (ok && n > 0) ok = tc::wait_warp(o_done + sub, (n - 1) & 1, &gave_up);
+    tc::fence_after();
+    asm volatile("bar.sync 2, %0;" ::"n"(256 + 32 * kFixWarps) : "memory");  // poison is known
+    const bool slow = poison != 0;
+    const int tok = it.q0 + row / g, h = kh * g + row % g;
+    if (sub < subs && ok) {
+      if (slow) {
+        if (mine)
+          slow_row<D>(p, split, tok, h, it.k0, min(kb * kTile, see), min(ke * kTile, see), see);
+      } else {
+        const RowOut dst = row_out(p, D, split, tok, h);
+        const float inv = see > 0 ? 1.f / l : 0.f;
+#pragma unroll
+        for (int x = 0; x < D; x += 32) {
+          uint32_t o[32];
+          if (n > 0) {
+            __syncwarp();
+            tc::tmem_ld32(o_addr + x, o);
+            tc::wait_ld();
+          }
+          if (n <= 0 || see == 0)
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = 0;
+          if (mine && p.splits == 1) {
+            uint4* out = reinterpret_cast<uint4*>(dst.out + x);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                w[z] = pack_bf16(__uint_as_float(o[8 * y + 2 * z]) * inv,
+                                 __uint_as_float(o[8 * y + 2 * z + 1]) * inv);
+              out[y] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (mine) {
+            uint4* out = reinterpret_cast<uint4*>(dst.o + x);
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              out[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            if (x == 0) *dst.ml = make_float2(m, see > kb * kTile && kb < ke ? l : -1.f);
+          }
+        }
+      }
     }
   }
-  __nv_bfloat16* o = p.out + t * p.a.out_row_stride + h * p.a.out_head_stride;
+  if (warp >= kFixWarp) asm volatile("bar.sync 2, %0;" ::"n"(256 + 32 * kFixWarps) : "memory");
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::fence_after();
+    tc::tmem_free(tmem, 512);
+  }
+  if (threadIdx.x == 0 && gave_up) atomicExch(p.status, TRE_ERR_DEP_TIMEOUT);
+}
+
+// Joins the parts of the rows of one item, a warp per row, parts in order.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
+  const int g = p.a.n_q_heads / p.a.n_kv_heads, kh = blockIdx.x % p.a.n_kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Item it = find_item(p, g, (int)(blockIdx.x / p.a.n_kv_heads));
+  const int rr = blockIdx.y * 8 + warp;
+  if (rr >= it.rows) return;
+  const int row = it.row0 + rr, tok = it.q0 + row / g, h = kh * g + row % g;
+  const int64_t step = (int64_t)p.a.n_q_rows * p.a.n_q_heads;
+  const int64_t at = (int64_t)tok * p.a.n_q_heads + h;
+  float m = -INFINITY;
+  bool seen = false;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[s * step + at];
+    seen |= ml.y != -1.f;
+    m = fmaxf(m, ml.x);
+  }
+  constexpr int E = D / 32;
+  float l = 0.f, acc[E] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[s * step + at];
+    if (ml.x == -INFINITY) continue;  // nothing but zeros
+    const float f = ml.x == m ? 1.f : exp2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    const float* o = p.part_o + (s * step + at) * D;
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j)
-    o[lane + 32 * j] = __float2bfloat16_rn(see > 0 ? acc[j] / l : 0.f);
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(o[lane + 32 * e], f, acc[e]);
+  }
+  __nv_bfloat16* out = p.out + (int64_t)tok * p.a.out_row_stride + (int64_t)h * p.a.out_head_stride;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[lane + 32 * e] = __float2bfloat16_rn(seen ? acc[e] / l : 0.f);
 }
 
 tre_status check(const char* op, const tre_attention* a) {
@@ -103,6 +543,57 @@ tre_status check(const char* op, const tre_attention* a) {
   return TRE_OK;
 }
 
+
+// Row tiles of a kv head: an upper bound, the lengths are known on the device only.
+int row_tiles(const tre_attention& a) {
+  const int64_t rows = (int64_t)a.n_q_rows * (a.n_q_heads / a.n_kv_heads);
+  if (a.n_seqs == 0) return (int)((rows + kItemRows - 1) / kItemRows);
+  return (int)(rows / kItemRows + std::min(a.n_seqs, a.n_q_rows));
+}
+
+// Parts along the keys: as many as fill the device when the rows alone do not, each of two
+// key tiles or more.
+int key_splits(const tre_attention& a, int sms) {
+  const int64_t items = (int64_t)row_tiles(a) * a.n_kv_heads;
+  const int64_t tiles = ((int64_t)a.n_kv_rows + kTile - 1) / kTile;
+  if (items == 0 || items * 2 > sms) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 2));
+}
+
+size_t workspace_bytes_of(const tre_attention& a, int sms) {
+  const int splits = key_splits(a, sms);
+  if (splits == 1) return 0;
+  return (size_t)splits * a.n_q_rows * a.n_q_heads * (a.head_dim * 4 + 8);
+}
+
+template <int D>
+tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
+                  const CUtensorMap& vmap, cudaStream_t stream) {
+  auto kernel = prompt_attention_kernel<D>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+  if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  const unsigned items = (unsigned)(p.tiles * p.a.n_kv_heads);
+  kernel<<<dim3(items, p.splits), kThreadsAttn, Shape<D>::kSmem, stream>>>(kmap, vmap, p);
+  if (p.splits > 1) {
+    const int most = (int)std::min<int64_t>(
+        kItemRows, (int64_t)p.a.n_q_rows * (p.a.n_q_heads / p.a.n_kv_heads));
+    join_kernel<D><<<dim3(items, (most + 7) / 8), 256, 0, stream>>>(p);
+  }
+  return op_launch_status(op);
+}
+
+tre_status map_of(const char* op, const void* base, int D, int64_t rows, int heads,
+                  int64_t row_stride, int64_t head_stride, CUtensorMap* out) {
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)rows, (uint64_t)heads};
+  // the stride of a dimension of one entry is never used, but has to be valid
+  const uint64_t st[2] = {(uint64_t)(rows > 1 ? row_stride : D) * 2,
+                          (uint64_t)(heads > 1 ? head_stride : D) * 2};
+  const uint32_t box[3] = {64, kTile, 1};
+  return encode_map(op, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, st, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, out);
+}
+
 }  // namespace
 }  // namespace tre
 
@@ -114,7 +605,7 @@ TRE_EXPORT tre_status tre_prompt_attention_workspace(const tre_attention* a, int
   const tre_status st = check(op, a);
   if (st != TRE_OK) return st;
   OP_ARG(bytes && num_sms > 0, op, "bad argument");
-  *bytes = 0;
+  *bytes = workspace_bytes_of(*a, num_sms);
   return TRE_OK;
 }
 
@@ -123,7 +614,7 @@ TRE_EXPORT tre_status tre_prompt_attention(const tre_attention* a, const void* q
                                            const int32_t* kv_offsets, void* out, void* workspace,
                                            size_t workspace_bytes, tre_stream stream) {
   static const char* op = "tre_prompt_attention";
-  const tre_status st = check(op, a);
+  tre_status st = check(op, a);
   if (st != TRE_OK) return st;
   if (a->n_q_rows == 0) return TRE_OK;
   OP_ARG(ptr16(q) && ptr16(out) && (a->n_kv_rows == 0 || (ptr16(k) && ptr16(v))), op,
@@ -131,13 +622,36 @@ TRE_EXPORT tre_status tre_prompt_attention(const tre_attention* a, const void* q
   OP_ARG(a->n_seqs == 0 || (q_offsets && kv_offsets && ((uintptr_t)q_offsets & 3) == 0 &&
                             ((uintptr_t)kv_offsets & 3) == 0),
          op, "sequences need offsets");
-  AttnParams p{*a, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-               static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(out), q_offsets,
-               kv_offsets};
-  const dim3 grid((unsigned)a->n_q_rows, (unsigned)((a->n_q_heads + kWarps - 1) / kWarps));
-  if (a->head_dim == 64)
-    prompt_attention_kernel<64><<<grid, kWarps * 32, 0, (cudaStream_t)stream>>>(p);
-  else
-    prompt_attention_kernel<128><<<grid, kWarps * 32, 0, (cudaStream_t)stream>>>(p);
-  return op_launch_status(op);
+  const int sms = device_sms();
+  const size_t need = workspace_bytes_of(*a, sms);
+  OP_ARG(need == 0 || (ptr16(workspace) && workspace_bytes >= need), op,
+         "the workspace is too small or misaligned");
+  AttnParams p{};
+  p.a = *a;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q_offsets = q_offsets;
+  p.kv_offsets = kv_offsets;
+  p.tiles = row_tiles(*a);
+  p.splits = key_splits(*a, sms);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o +
+                                        (size_t)p.splits * a->n_q_rows * a->n_q_heads * a->head_dim);
+  p.c = a->scale * 1.4426950408889634f;
+  p.status = ops_status_ptr();
+  OP_ARG(p.status, op, "the operators' status word is not available");
+  OP_ARG((int64_t)p.tiles * a->n_kv_heads < ((int64_t)1 << 31), op, "too many query rows");
+  CUtensorMap kmap{}, vmap{};
+  if (a->n_kv_rows > 0) {
+    st = map_of(op, k, a->head_dim, a->n_kv_rows, a->n_kv_heads, a->k_row_stride,
+                a->k_head_stride, &kmap);
+    if (st == TRE_OK)
+      st = map_of(op, v, a->head_dim, a->n_kv_rows, a->n_kv_heads, a->v_row_stride,
+                  a->v_head_stride, &vmap);
+    if (st != TRE_OK) return st;
+  }
+  return a->head_dim == 64 ? launch<64>(op, p, kmap, vmap, (cudaStream_t)stream)
+                           : launch<128>(op, p, kmap, vmap, (cudaStream_t)stream);
 }
