@@ -344,9 +344,9 @@ tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap
                   const CUtensorMap& wmap, cudaStream_t stream) {
   using T = Tile<N>;
   auto kernel = mxfp4_matmul_kernel<N, Out>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
-  if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  static std::atomic<uint64_t> devices;
+  if (!allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem, &devices))
+    return op_error(TRE_ERR_CUDA, op, "the device refuses the kernel's shared memory");
   cudaLaunchConfig_t c = {};
   const int64_t tiles = p.offsets ? (int64_t)p.rows / N + std::min<int64_t>(p.n_experts, p.rows)
                                   : ((int64_t)p.rows + N - 1) / N;
@@ -361,7 +361,7 @@ tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   c.attrs = &attr;
   c.numAttrs = p.splits > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&c, kernel, xmap, wmap, p);
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, xmap, wmap, p);
   return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
 }
 

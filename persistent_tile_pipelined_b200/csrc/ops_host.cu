@@ -7,18 +7,51 @@ namespace tre {
 // One word per device: the module's copy on the current one.
 __device__ int32_t g_ops_status;
 
+namespace {
+
+constexpr int kDevices = 64;
+
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : -1;
+}
+
+}  // namespace
+
 int32_t* ops_status_ptr() {
-  void* p = nullptr;
-  return cudaGetSymbolAddress(&p, g_ops_status) == cudaSuccess ? static_cast<int32_t*>(p)
-                                                               : nullptr;
+  static std::atomic<int32_t*> known[kDevices];
+  const int dev = current_device();
+  if (dev < 0) return nullptr;
+  int32_t* at = known[dev].load(std::memory_order_relaxed);
+  if (!at) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_ops_status) != cudaSuccess) return nullptr;
+    known[dev].store(at = static_cast<int32_t*>(p), std::memory_order_relaxed);
+  }
+  return at;
 }
 
 int device_sms() {
-  static int sms[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!sms[dev]) cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-  return sms[dev] > 0 ? sms[dev] : 148;
+  static std::atomic<int> known[kDevices];
+  const int dev = current_device();
+  if (dev < 0) return 148;
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (!sms) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 148;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
+}
+
+bool allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* devices) {
+  const int dev = current_device();
+  if (dev < 0) return false;
+  if (devices->load(std::memory_order_relaxed) >> dev & 1) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  devices->fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return true;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

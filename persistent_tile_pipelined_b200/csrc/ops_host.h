@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <string>
 
 #include "tre_internal.h"
@@ -28,6 +29,10 @@ int device_sms();
 // Device address of the status word that tre_ops_status reports (NULL when the module
 // cannot be loaded).
 int32_t* ops_status_ptr();
+
+// Allow `kernel` its dynamic shared memory on the current device, once per device
+// (`devices`: the kernel's own record of where that is done).
+bool allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* devices);
 
 }  // namespace tre
 

@@ -121,35 +121,48 @@ __device__ __forceinline__ RowOut row_out(const AttnParams& p, int D, int split,
           p.part_o + at * D, p.part_ml + at};
 }
 
-// One row the long way, by one thread: keys [from, to) of the sequence in order.  Taken by
-// every row of a CTA whose partly visible key tiles hold a NaN or an infinity in v: the matrix
-// product would carry 0 x NaN into rows that do not see the key.
+// One row the long way, by one warp: keys [from, to) of the sequence in order, the lanes
+// sharing the width.  Taken by every row of a CTA whose partly visible key tiles hold a NaN or
+// an infinity in v: the matrix product would carry 0 x NaN into rows that do not see the key.
 template <int D>
-__device__ __noinline__ void slow_row(const AttnParams& p, int split, int tok, int h, int k0,
-                                      int from, int to, int see) {
-  const int kh = h / (p.a.n_q_heads / p.a.n_kv_heads);
-  const __nv_bfloat16* q = p.q + (int64_t)tok * p.a.q_row_stride + (int64_t)h * p.a.q_head_stride;
-  float acc[D], m = -INFINITY, l = 0.f;
-  for (int d = 0; d < D; ++d) acc[d] = 0.f;
+__device__ __forceinline__ void slow_row(const AttnParams& p, int split, int tok, int h, int k0,
+                                         int from, int to, int see) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, kh = h / (p.a.n_q_heads / p.a.n_kv_heads);
+  const __nv_bfloat16* qr =
+      p.q + (int64_t)tok * p.a.q_row_stride + (int64_t)h * p.a.q_head_stride + lane;
+  const __nv_bfloat16* k = p.k + (int64_t)kh * p.a.k_head_stride + lane;
+  const __nv_bfloat16* v = p.v + (int64_t)kh * p.a.v_head_stride + lane;
+  float q[E], acc[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(qr[32 * e]), acc[e] = 0.f;
+#pragma unroll 1
   for (int s = from; s < to; ++s) {
-    const __nv_bfloat16* k =
-        p.k + (int64_t)kh * p.a.k_head_stride + (int64_t)(k0 + s) * p.a.k_row_stride;
-    const __nv_bfloat16* v =
-        p.v + (int64_t)kh * p.a.v_head_stride + (int64_t)(k0 + s) * p.a.v_row_stride;
-    float dot = 0.f;
-    for (int d = 0; d < D; ++d) dot = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), dot);
-    const float x = dot * p.c, mn = fmaxf(m, x), sh = mn == -INFINITY ? 0.f : mn;
-    const float old = m == mn ? 1.f : exp2_approx(m - sh), e = exp2_approx(x - sh);
-    for (int d = 0; d < D; ++d) acc[d] = fmaf(e, __bfloat162float(v[d]), acc[d] * old);
-    l = fmaf(l, old, e);
+    const int64_t at = k0 + s;
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      x = fmaf(q[e], __bfloat162float(k[at * p.a.k_row_stride + 32 * e]), x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    x *= p.c;
+    const float mn = fmaxf(m, x), sh = mn == -INFINITY ? 0.f : mn;
+    const float old = m == mn ? 1.f : exp2_approx(m - sh), w = exp2_approx(x - sh);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      acc[e] = fmaf(w, __bfloat162float(v[at * p.a.v_row_stride + 32 * e]), acc[e] * old);
+    l = fmaf(l, old, w);
     m = mn;
   }
   const RowOut r = row_out(p, D, split, tok, h);
   if (p.splits > 1) {
-    for (int d = 0; d < D; ++d) r.o[d] = acc[d];
-    *r.ml = make_float2(m, to > from ? l : -1.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) r.o[lane + 32 * e] = acc[e];
+    if (lane == 0) *r.ml = make_float2(m, to > from ? l : -1.f);
   } else {
-    for (int d = 0; d < D; ++d) r.out[d] = __float2bfloat16_rn(see > 0 ? acc[d] / l : 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      r.out[lane + 32 * e] = __float2bfloat16_rn(see > 0 ? acc[e] / l : 0.f);
   }
 }
 
@@ -228,6 +241,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   n_sub[0] = min(n_sub[0], ke);
   n_sub[1] = min(n_sub[1], ke);
 
+  // Registers: 384 threads x 168 at launch; the softmax warps hold a row of scores (256 x 208)
+  // and the others give theirs up (128 x 80).
+  if (warp >= kCopyWarp) tc::regs_less<80>();
   if (warp == kCopyWarp) {
     if (tc::elect_one()) {
       int n = 0;
@@ -275,12 +291,14 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         tc::commit(o_done + sub);
       };
       if (kb < ke) {
-        for (int sub = 0; sub < subs; ++sub)
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
           if (kb < n_sub[sub]) ok = ok && tc::wait(q_full + sub, 0, &gave_up);
         tile_wait(0);
         if (ok) {
           tc::fence_after();
-          for (int sub = 0; sub < subs; ++sub)
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
             if (kb < n_sub[sub]) scores(sub, 0);
           tc::commit(empty + 0);
         }
@@ -292,11 +310,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         const bool partly = (i + 1) * kTile > least;
         if (partly && ok) mbar_arrive(v_check);
         if (i + 1 < ke) tile_wait(nk2);
-        for (int sub = 0; sub < subs && ok; ++sub) {
-          if (i >= n_sub[sub]) continue;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          if (i >= n_sub[sub] || !ok) continue;
           ok = tc::wait(p_full + sub, (i - kb) & 1, &gave_up) &&
                (!partly || tc::wait(v_fixed, fixed & 1, &gave_up));
-          if (!ok) break;
+          if (!ok) continue;
           tc::fence_after();
           outputs(sub, nv, i > kb);
           if (i + 1 < n_sub[sub]) scores(sub, nk2);
@@ -341,11 +360,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     }
     if (bad) poison = 1;
   } else {
+    tc::regs_more<208>();
     const int sub = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const int row = it.row0 + sub * kTile + r;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_addr = lane_addr + sub * kTile, o_addr = lane_addr + T::kO + sub * D;
-    if (sub < subs && kb < n_sub[sub]) {
+    if (sub < subs && kb < (sub == 0 ? n_sub[0] : n_sub[1])) {
       // this tile's rows of q, 16 bytes a lane, swizzled; rows that do not exist are zero
       constexpr int kChunks = D / 8;
       for (int x = r; x < kTile * kChunks; x += kTile) {
@@ -369,7 +389,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     const float c = p.c;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int i = kb; i < n_sub[sub]; ++i) {
+    const int n_mine = sub == 0 ? n_sub[0] : n_sub[1];
+    for (int i = kb; i < n_mine; ++i) {
       ok = tc::wait_warp(s_full + sub, (i - kb) & 1, &gave_up);
       if (!ok) break;
       tc::fence_after();
@@ -407,17 +428,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         }
       }
       const float shift = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 cc = make_float2(c, c), ms = make_float2(-shift, -shift);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int x = 0; x < kTile; x += 64) {
         uint32_t pk[32];
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
-          const float a = exp2_approx(fmaf(__uint_as_float(s[x + 2 * y]), c, -shift));
-          const float b = exp2_approx(fmaf(__uint_as_float(s[x + 2 * y + 1]), c, -shift));
-          sum[y & 1] += a;
-          sum[2 + (y & 1)] += b;
-          pk[y] = pack_bf16(a, b);
+          float2 e = tc::fma2(make_float2(__uint_as_float(s[x + 2 * y]),
+                                          __uint_as_float(s[x + 2 * y + 1])), cc, ms);
+          e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+          sum[y & 1] = tc::add2(sum[y & 1], e);
+          pk[y] = pack_bf16(e.x, e.y);
         }
         tc::tmem_st32(s_addr + x / 2, pk);
       }
@@ -425,10 +447,10 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + sub);
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     // the row's m and l stay in registers for the end
-    const int n = n_sub[sub] - kb;
+    const int n = n_mine - kb;
     if (ok && n > 0) ok = tc::wait_warp(o_done + sub, (n - 1) & 1, &gave_up);
     tc::fence_after();
     asm volatile("bar.sync 2, %0;" ::"n"(256 + 32 * kFixWarps) : "memory");  // poison is known
@@ -436,8 +458,13 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     const int tok = it.q0 + row / g, h = kh * g + row % g;
     if (sub < subs && ok) {
       if (slow) {
-        if (mine)
-          slow_row<D>(p, split, tok, h, it.k0, min(kb * kTile, see), min(ke * kTile, see), see);
+#pragma unroll 1
+        for (int x = 0; x < 32; ++x) {
+          const int rx = row - lane + x, sx = sees(rx);
+          if (rx - it.row0 >= it.rows) break;
+          slow_row<D>(p, split, it.q0 + rx / g, kh * g + rx % g, it.k0, min(kb * kTile, sx),
+                      min(ke * kTile, sx), sx);
+        }
       } else {
         const RowOut dst = row_out(p, D, split, tok, h);
         const float inv = see > 0 ? 1.f / l : 0.f;
@@ -570,9 +597,9 @@ template <int D>
 tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
                   const CUtensorMap& vmap, cudaStream_t stream) {
   auto kernel = prompt_attention_kernel<D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
-  if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  static std::atomic<uint64_t> devices;
+  if (!allow_smem(reinterpret_cast<const void*>(kernel), Shape<D>::kSmem, &devices))
+    return op_error(TRE_ERR_CUDA, op, "the device refuses the kernel's shared memory");
   const unsigned items = (unsigned)(p.tiles * p.a.n_kv_heads);
   kernel<<<dim3(items, p.splits), kThreadsAttn, Shape<D>::kSmem, stream>>>(kmap, vmap, p);
   if (p.splits > 1) {

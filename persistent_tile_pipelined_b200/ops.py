@@ -20,21 +20,29 @@ from .synth import mxfp4_pitch
 _TYPES = {torch.bfloat16: tre.TRE_BF16, torch.float32: tre.TRE_F32}
 
 
+_SMS = {}  # device index -> SM count
+
+
 def _need(cond: bool, what: str) -> None:
     if not cond:
         raise ValueError(what)
 
 
 def _tensor(t, name: str, ndim: int, dtypes, device=None) -> None:
-    _need(isinstance(t, torch.Tensor), f"{name} must be a tensor")
-    _need(t.ndim == ndim, f"{name} must have {ndim} dimensions, not {t.ndim}")
-    _need(t.dtype in dtypes, f"{name} has type {t.dtype}")
-    _need(t.is_cuda, f"{name} must be on a CUDA device")
-    _need(device is None or t.device == device, f"{name} is on {t.device}, not on {device}")
-    _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1,
-          f"{name}'s last dimension must be contiguous")
-    _need(not (t.requires_grad and torch.is_grad_enabled()),
-          f"{name} requires a gradient: the operator has no backward pass")
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.ndim != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, not {t.ndim}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1 and t.numel():
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient: the operator has no backward pass")
 
 
 def _span(t) -> Tuple[int, int]:
@@ -53,8 +61,27 @@ def _apart(out, name: str, /, **inputs) -> None:
             _need(b <= c or d <= a, f"{name} may not overlap {key}")
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, device, *args) -> None:
+    """fn(*args, current stream) with `device` current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != tre.TRE_OK:
+        raise tre.TreError(status, fn.__name__)
+
+
+def _sms(device) -> int:
+    n = _SMS.get(device.index)
+    if n is None:
+        n = _SMS[device.index] = torch.cuda.get_device_properties(device).multi_processor_count
+    return n
 
 
 def _offsets(t, name: str, device) -> None:
@@ -98,14 +125,10 @@ def prompt_attention(q, k, v, q_offsets=None, kv_offsets=None, scale: Optional[f
     a = tre.tre_attention(Hq, Hkv, D, n, T, S, q.stride(0), q.stride(1), k.stride(1), k.stride(0),
                           v.stride(1), v.stride(0), out.stride(0), out.stride(1),
                           1.0 / math.sqrt(D) if scale is None else scale)
-    sms = torch.cuda.get_device_properties(q.device).multi_processor_count
-    need = tre.tre_prompt_attention_workspace(a, sms)
-    with torch.cuda.device(q.device):
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        tre.check(tre.tre_prompt_attention(
-            a, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr() if n else 0,
-            kv_offsets.data_ptr() if n else 0, out.data_ptr(), ws.data_ptr() if need else 0, need,
-            _stream(q.device)), "tre_prompt_attention")
+    need = tre.tre_prompt_attention_workspace(a, _sms(q.device))
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _call(tre.lib.tre_prompt_attention, q.device, a, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _ptr(q_offsets), _ptr(kv_offsets), out.data_ptr(), _ptr(ws), need)
     return out
 
 
@@ -127,10 +150,8 @@ def mxfp4_quantize(w, out=None):
         _need(tuple(out.shape) == shape and out.is_contiguous(),
               f"out must be contiguous and of shape {shape}")
         _apart(out, "out", w=flat)
-    with torch.cuda.device(w.device):
-        tre.check(tre.tre_mxfp4_quantize(flat.data_ptr(), _TYPES[w.dtype], R, K, flat.stride(0),
-                                         out.data_ptr(), _stream(w.device)),
-                  "tre_mxfp4_quantize")
+    _call(tre.lib.tre_mxfp4_quantize, w.device, flat.data_ptr(), _TYPES[w.dtype], R, K,
+          flat.stride(0), out.data_ptr())
     return out
 
 
@@ -156,10 +177,8 @@ def mxfp4_dequantize(w, k: int, out_dtype=torch.bfloat16, out=None):
         _need(tuple(out.shape) == shape and out.is_contiguous(),
               f"out must be contiguous and of shape {shape}")
         _apart(out, "out", w=w)
-    with torch.cuda.device(w.device):
-        tre.check(tre.tre_mxfp4_dequantize(w.data_ptr(), w.numel() // w.shape[-1], k,
-                                           _TYPES[out_dtype], out.data_ptr(), _stream(w.device)),
-                  "tre_mxfp4_dequantize")
+    _call(tre.lib.tre_mxfp4_dequantize, w.device, w.data_ptr(), w.numel() // w.shape[-1], k,
+          _TYPES[out_dtype], out.data_ptr())
     return out
 
 
@@ -190,11 +209,8 @@ def mxfp4_matmul(x, w, offsets=None, out_dtype=torch.float32, out=None):
         _tensor(out, "out", 2, (out_dtype,), x.device)
         _need(tuple(out.shape) == (T, N), f"out has shape {tuple(out.shape)}")
         _apart(out, "out", x=x, w=w, offsets=offsets)
-    with torch.cuda.device(x.device):
-        tre.check(tre.tre_mxfp4_matmul(
-            x.data_ptr(), x.stride(0), w.data_ptr(), offsets.data_ptr() if offsets is not None
-            else 0, E, T, N, K, _TYPES[out_dtype], out.data_ptr(), out.stride(0),
-            _stream(x.device)), "tre_mxfp4_matmul")
+    _call(tre.lib.tre_mxfp4_matmul, x.device, x.data_ptr(), x.stride(0), w.data_ptr(),
+          _ptr(offsets), E, T, N, K, _TYPES[out_dtype], out.data_ptr(), out.stride(0))
     return out
 
 
@@ -210,25 +226,24 @@ def add_rmsnorm(x, delta, gain, eps: float, x_out=None, out=None):
         _need(delta.shape == x.shape, f"delta has shape {tuple(delta.shape)}")
     _tensor(gain, "gain", 1, (torch.bfloat16,), x.device)
     _need(gain.shape[0] == d, f"gain has {gain.shape[0]} entries, not {d}")
-    if x_out is None:
+    own_x, own = x_out is None, out is None
+    if own_x:
         x_out = torch.empty((T, d), dtype=torch.float32, device=x.device)
     elif x_out is not x:
         _tensor(x_out, "x_out", 2, (torch.float32,), x.device)
         _need(x_out.shape == x.shape, f"x_out has shape {tuple(x_out.shape)}")
         if x_out.data_ptr() != x.data_ptr() or x_out.stride() != x.stride():
             _apart(x_out, "x_out", x=x)
-    if out is None:
+    if own:
         out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
     else:
         _tensor(out, "out", 2, (torch.bfloat16,), x.device)
         _need(out.shape == x.shape, f"out has shape {tuple(out.shape)}")
-    _apart(x_out, "x_out", delta=delta, gain=gain, out=out)
-    _apart(out, "out", x=x, delta=delta, gain=gain)
-    with torch.cuda.device(x.device):
-        tre.check(tre.tre_add_rmsnorm(
-            x.data_ptr(), x.stride(0), delta.data_ptr() if delta is not None else 0,
-            _TYPES[delta.dtype] if delta is not None else 0,
-            delta.stride(0) if delta is not None else 0, gain.data_ptr(), eps, T, d,
-            x_out.data_ptr(), x_out.stride(0), out.data_ptr(), out.stride(0), _stream(x.device)),
-            "tre_add_rmsnorm")
+        _apart(out, "out", x=x, delta=delta, gain=gain)
+    if not own_x:
+        _apart(x_out, "x_out", delta=delta, gain=gain, out=None if own else out)
+    _call(tre.lib.tre_add_rmsnorm, x.device, x.data_ptr(), x.stride(0), _ptr(delta),
+          0 if delta is None else _TYPES[delta.dtype], 0 if delta is None else delta.stride(0),
+          gain.data_ptr(), eps, T, d, x_out.data_ptr(), x_out.stride(0), out.data_ptr(),
+          out.stride(0))
     return x_out, out
