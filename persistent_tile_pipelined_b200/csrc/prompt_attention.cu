@@ -102,6 +102,33 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// The larger of three; NaN if any is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 2^x of two numbers below 128 on the fused multiply-add units: x = i + f with |f| <= 1/2,
+// 2^f by the cubic of least relative error (9e-5 = 2^-13; its constant is 1, so that x <= -127
+// gives exact zero), i added to the exponent bits.  Not for NaN.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  const float2 magic = make_float2(12582912.f, 12582912.f);  // 1.5 x 2^23: x rounds to i
+  const float2 minus = make_float2(-12582912.f, -12582912.f);
+  const float2 none = make_float2(-1.f, -1.f);
+  x.x = fmaxf(x.x, -127.f);
+  x.y = fmaxf(x.y, -127.f);
+  const float2 t = tc::add2(x, magic);
+  const float2 f = tc::fma2(tc::add2(t, minus), none, x);
+  float2 q = tc::fma2(f, make_float2(0.05500893f, 0.05500893f),
+                      make_float2(0.24221096f, 0.24221096f));
+  q = tc::fma2(q, f, make_float2(0.69328293f, 0.69328293f));
+  q = tc::fma2(q, f, make_float2(1.f, 1.f));
+  return make_float2(
+      __uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -341,9 +368,13 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       // could mistake an earlier round of the ring for this one)
       if (!tc::wait_warp(v_check, checked++ & 1, &gave_up)) break;
       uint8_t* v = ring + (2 * (i - kb) + 1) % T::ST * T::kTileBytes;
-      for (int j = max(least - i * kTile, 0) + warp - kFixWarp; j < kTile; j += kFixWarps) {
-        if (lane >= D / 8) continue;
-        uint4* at = reinterpret_cast<uint4*>(v + (lane >> 3) * kTile * 128 + j * 128 + (lane & 7) * 16);
+      constexpr int kLanes = D / 8, kRowsAtOnce = kFixWarps * 32 / kLanes;
+      const int t64 = threadIdx.x - kFixWarp * 32, ch = t64 % kLanes;
+      const int from = max(least - i * kTile, 0) / kRowsAtOnce * kRowsAtOnce;
+      v += (ch >> 3) * kTile * 128 + (ch & 7) * 16;
+#pragma unroll 4
+      for (int j = from + t64 / kLanes; j < kTile; j += kRowsAtOnce) {
+        uint4* at = reinterpret_cast<uint4*>(v + j * 128);
         if (i * kTile + j >= it.nk) {
           *at = make_uint4(0, 0, 0, 0);
         } else {
@@ -367,17 +398,28 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     const uint32_t s_addr = lane_addr + sub * kTile, o_addr = lane_addr + T::kO + sub * D;
     if (sub < subs && kb < (sub == 0 ? n_sub[0] : n_sub[1])) {
       // this tile's rows of q, 16 bytes a lane, swizzled; rows that do not exist are zero
-      constexpr int kChunks = D / 8;
-      for (int x = r; x < kTile * kChunks; x += kTile) {
-        const int rr = x / kChunks, ch = x % kChunks, gr = sub * kTile + rr;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (gr < it.rows) {
-          const int tok = it.q0 + (it.row0 + gr) / g, h = kh * g + (it.row0 + gr) % g;
-          val = *reinterpret_cast<const uint4*>(p.q + (int64_t)tok * p.a.q_row_stride +
-                                                (int64_t)h * p.a.q_head_stride + ch * 8);
+      constexpr int kChunks = D / 8, kPass = kTile / kChunks, kBatch = 8;
+      const int ch = r % kChunks, r8 = r / kChunks;
+      uint8_t* dst = qs + sub * T::kTileBytes + (ch >> 3) * kTile * 128;
+#pragma unroll
+      for (int x = 0; x < kChunks; x += kBatch) {
+        uint4 val[kBatch];  // loads in flight together
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          const int gr = sub * kTile + r8 + (x + y) * kPass;
+          val[y] = make_uint4(0, 0, 0, 0);
+          if (gr < it.rows) {
+            const uint32_t at = (uint32_t)(it.row0 + gr), tk = at / (uint32_t)g;
+            val[y] = *reinterpret_cast<const uint4*>(
+                p.q + (int64_t)(it.q0 + (int)tk) * p.a.q_row_stride +
+                (int64_t)(kh * g + (int)(at - tk * g)) * p.a.q_head_stride + ch * 8);
+          }
         }
-        *reinterpret_cast<uint4*>(qs + sub * T::kTileBytes + (ch >> 3) * kTile * 128 + rr * 128 +
-                                  (((ch & 7) ^ (rr & 7)) * 16)) = val;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          const int rr = r8 + (x + y) * kPass;
+          *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) * 16)) = val[y];
+        }
       }
       tc::fence_async_smem();
       __syncwarp();
@@ -406,8 +448,15 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int x = 0; x < kTile; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
-      const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
+      for (int x = 0; x < kTile; x += 8)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          mx[y] = max3_nan(mx[y], __uint_as_float(s[x + 2 * y]), __uint_as_float(s[x + 2 * y + 1]));
+      float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * c;
+      // a NaN or an infinite score makes the row NaN (infinity less itself): by its sum, since
+      // the exponentials below need not carry it
+      if (!(top < INFINITY)) l = NAN, top = m;
+      top = fmaxf(m, top);
       if (__any_sync(0xffffffffu, top > m + kRaise || (i == kb))) {
         const float f = top == m ? 1.f : exp2_approx(m - top);
         m = top;
@@ -437,7 +486,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         for (int y = 0; y < 32; ++y) {
           float2 e = tc::fma2(make_float2(__uint_as_float(s[x + 2 * y]),
                                           __uint_as_float(s[x + 2 * y + 1])), cc, ms);
-          e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+          // a quarter of them on the multiply-add units: the special-function unit alone (16 a
+          // clock) takes as long as both matrix products of the tile
+          e = (y & 3) == 3 ? exp2_poly(e) : make_float2(exp2_approx(e.x), exp2_approx(e.y));
           sum[y & 1] = tc::add2(sum[y & 1], e);
           pk[y] = pack_bf16(e.x, e.y);
         }
