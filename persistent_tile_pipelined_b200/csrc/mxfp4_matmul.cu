@@ -49,19 +49,17 @@ struct MatmulParams {
 
 // The bf16 pairs of 8 codes (a little-endian word: element 2i in the low nibble of byte i),
 // unscaled: the code's exponent and mantissa bits sit in bf16's lowest exponent and highest
-// mantissa bits, which is the number times 2^-126 (its subnormal 0.5 included).  Both bytes
-// of each half come from whole-word shifts and masks, then byte permutes pair them.
+// mantissa bits, which is the number times 2^-126 (its subnormal 0.5 included).  A byte
+// permute doubles the nibble's byte into both bytes of its half, once shifted so that both
+// nibbles stand high: the sign is then in place and the magnitude two bits below its own.
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t* o) {
-  const uint32_t he = ((w << 4) & 0x80808080u) | ((w >> 2) & 0x01010101u);  // even, high bytes
-  const uint32_t le = (w << 6) & 0xc0c0c0c0u;
-  const uint32_t ho = (w & 0x80808080u) | ((w >> 6) & 0x01010101u);
-  const uint32_t lo = (w << 2) & 0xc0c0c0c0u;
-  const uint32_t e01 = __byte_perm(le, he, 0x5140), e23 = __byte_perm(le, he, 0x7362);
-  const uint32_t o01 = __byte_perm(lo, ho, 0x5140), o23 = __byte_perm(lo, ho, 0x7362);
-  o[0] = __byte_perm(e01, o01, 0x5410);
-  o[1] = __byte_perm(e01, o01, 0x7632);
-  o[2] = __byte_perm(e23, o23, 0x5410);
-  o[3] = __byte_perm(e23, o23, 0x7632);
+  const uint32_t w4 = w << 4;
+  constexpr uint32_t sel[4] = {0x4400, 0x5511, 0x6622, 0x7733};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = __byte_perm(w4, w, sel[i]);
+    o[i] = (p & 0x80008000u) | ((p << 2) & 0x01c001c0u);
+  }
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -365,10 +363,10 @@ tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap
   return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
 }
 
-// Rows of x per tile: the least of 16 .. 256 that covers twice an expert's average (most
-// experts' weights pass once), but no more than leaves the device without tiles to fill it.
+// Rows of x per tile: the least of 16 .. 256 that covers three times an expert's average (few
+// experts' weights are decoded twice), but no more than leaves the device without tiles to fill it.
 int tile_rows(const MatmulParams& p, int sms) {
-  const int64_t avg = ((int64_t)p.rows * (p.n_experts > 1 ? 2 : 1) + p.n_experts - 1) / p.n_experts;
+  const int64_t avg = ((int64_t)p.rows * (p.n_experts > 1 ? 3 : 1) + p.n_experts - 1) / p.n_experts;
   int best = 16;
   while (best < 256 && best < avg) best *= 2;
   const int64_t row_tiles = (p.n + kRows - 1) / kRows;

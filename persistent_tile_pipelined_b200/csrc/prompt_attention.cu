@@ -30,8 +30,9 @@ constexpr float kRaise = 8.f;                  // log2 of how far P may exceed 1
 template <int D>
 struct Shape {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int ST = D == 128 ? 5 : 10;  // key and value tiles in flight
-  static constexpr int kSmem = 2 * kTileBytes + ST * kTileBytes + 1024 + 256;
+  static constexpr int ST = D == 128 ? 5 : 10;  // key and value tiles in flight (one more
+                                                // where the second row tile's q is not needed)
+  static constexpr int kSmem = (2 + ST) * kTileBytes + 1024 + 512;
   static constexpr int kO = 2 * kTile;          // tensor-memory column of the first O
 };
 
@@ -201,10 +202,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
-  uint8_t* ring = qs + 2 * T::kTileBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + T::ST * T::kTileBytes);
-  uint64_t* empty = full + T::ST;
-  uint64_t* q_full = empty + T::ST;
+  uint64_t* full = reinterpret_cast<uint64_t*>(qs + (2 + T::ST) * T::kTileBytes);
+  uint64_t* empty = full + T::ST + 1;
+  uint64_t* q_full = empty + T::ST + 1;
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       poison = 0;
     }
   } else if (warp == 1 && lane == 0) {
-    for (int i = 0; i < T::ST; ++i) {
+    for (int i = 0; i < T::ST + 1; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
     }
@@ -265,8 +265,16 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   const int split = blockIdx.y;
   const int kb = (int)((int64_t)n_all * split / p.splits);
   const int ke = (int)((int64_t)n_all * (split + 1) / p.splits);
+  // One row tile alone would wait for its own softmax at every step: both take it, with the
+  // even and the odd key tiles, and join their sums at the end.
+  const bool alternate = subs == 1;
   n_sub[0] = min(n_sub[0], ke);
-  n_sub[1] = min(n_sub[1], ke);
+  n_sub[1] = alternate ? n_sub[0] : min(n_sub[1], ke);
+
+  uint8_t* ring = qs + (alternate ? 1 : 2) * T::kTileBytes;
+  // the n-th copy's place and how often that was used before: K and V tiles in turn
+  auto slot_of = [&](int n) { return alternate ? n % (T::ST + 1) : n % T::ST; };
+  auto round_of = [&](int n) { return alternate ? n / (T::ST + 1) : n / T::ST; };
 
   // Registers: 384 threads x 168 at launch; the softmax warps hold a row of scores (256 x 208)
   // and the others give theirs up (128 x 80).
@@ -276,8 +284,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       int n = 0;
       const int total = 2 * (ke - kb);
       for (; n < total; ++n) {
-        const int slot = n % T::ST;
-        if (!tc::wait(empty + slot, (n / T::ST & 1) ^ 1, &gave_up)) break;
+        const int slot = slot_of(n);
+        if (!tc::wait(empty + slot, (round_of(n) & 1) ^ 1, &gave_up)) break;
         uint8_t* dst = ring + slot * T::kTileBytes;
         mbar_arrive_expect_tx(full + slot, T::kTileBytes);
         const int row = it.k0 + (kb + n / 2) * kTile;
@@ -286,8 +294,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
           tc::load_3d(dst + h * kTile * 128, n & 1 ? &vmap : &kmap, h * 64, row, kh, full + slot);
       }
       if (gave_up)  // copies in flight land before the CTA ends
-        for (int i = max(0, n - T::ST); i < n; ++i)
-          for (int x = 0; x < 100000 && !mbar_try_wait(full + i % T::ST, i / T::ST & 1); ++x) {
+        for (int i = max(0, n - T::ST - 1); i < n; ++i)
+          for (int x = 0; x < 100000 && !mbar_try_wait(full + slot_of(i), round_of(i) & 1); ++x) {
           }
     }
   } else if (warp == kMmaWarp) {
@@ -296,11 +304,11 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       constexpr uint32_t id_o = tc::idesc_bf16(kTile, D, 1);
       bool ok = true;
       auto tile_wait = [&](int n) {
-        ok = ok && tc::wait(full + n % T::ST, n / T::ST & 1, &gave_up);
+        ok = ok && tc::wait(full + slot_of(n), round_of(n) & 1, &gave_up);
       };
       auto scores = [&](int sub, int n) {
-        const uint32_t q = smem_u32(qs + sub * T::kTileBytes);
-        const uint32_t k = smem_u32(ring + n % T::ST * T::kTileBytes);
+        const uint32_t q = smem_u32(qs + (alternate ? 0 : sub * T::kTileBytes));
+        const uint32_t k = smem_u32(ring + slot_of(n) * T::kTileBytes);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           const uint32_t at = (j / 4) * kTile * 128 + (j % 4) * 32;
@@ -310,47 +318,55 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         tc::commit(s_full + sub);
       };
       auto outputs = [&](int sub, int n, bool add) {
-        const uint32_t v = smem_u32(ring + n % T::ST * T::kTileBytes);
+        const uint32_t v = smem_u32(ring + slot_of(n) * T::kTileBytes);
 #pragma unroll
         for (int j = 0; j < kTile / 16; ++j)
           tc::mma_ts(tmem + T::kO + sub * D, tmem + sub * kTile + j * 8,
                      tc::smem_desc(v + j * 2048, kTile * 128, 1024), id_o, add || j > 0);
         tc::commit(o_done + sub);
       };
-      if (kb < ke) {
+      // alternating: tile i of the keys belongs to row tile (i - kb) mod 2, whose S follows two
+      // key tiles ahead of its O; else both row tiles take every key tile, S one ahead
+      const int ahead = alternate ? 2 : 1;
+      auto takes = [&](int sub, int i) {
+        return i < n_sub[sub] && (!alternate || ((i - kb) & 1) == sub);
+      };
+      for (int i = kb; i < min(kb + ahead, ke) && ok; ++i) {
+        tile_wait(2 * (i - kb));
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-          if (kb < n_sub[sub]) ok = ok && tc::wait(q_full + sub, 0, &gave_up);
-        tile_wait(0);
-        if (ok) {
+        for (int sub = 0; sub < 2; ++sub) {
+          if (!ok || !takes(sub, i)) continue;
+          if (i == kb || alternate) ok = tc::wait(q_full + (alternate ? 0 : sub), 0, &gave_up);
+          if (!ok) continue;
           tc::fence_after();
-#pragma unroll
-          for (int sub = 0; sub < 2; ++sub)
-            if (kb < n_sub[sub]) scores(sub, 0);
-          tc::commit(empty + 0);
+          scores(sub, 2 * (i - kb));
         }
+        tc::commit(empty + slot_of(2 * (i - kb)));
       }
       int fixed = 0;
       for (int i = kb; i < ke && ok; ++i) {
-        const int nv = 2 * (i - kb) + 1, nk2 = nv + 1;
+        const int nv = 2 * (i - kb) + 1, next = i + ahead, nk2 = 2 * (next - kb);
         tile_wait(nv);
         const bool partly = (i + 1) * kTile > least;
         if (partly && ok) mbar_arrive(v_check);
-        if (i + 1 < ke) tile_wait(nk2);
+        const int round = alternate ? (i - kb) >> 1 : i - kb;
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-          if (i >= n_sub[sub] || !ok) continue;
-          ok = tc::wait(p_full + sub, (i - kb) & 1, &gave_up) &&
+          if (!takes(sub, i) || !ok) continue;
+          ok = tc::wait(p_full + sub, round & 1, &gave_up) &&
                (!partly || tc::wait(v_fixed, fixed & 1, &gave_up));
           if (!ok) continue;
           tc::fence_after();
-          outputs(sub, nv, i > kb);
-          if (i + 1 < n_sub[sub]) scores(sub, nk2);
+          outputs(sub, nv, round > 0);
+          if (takes(sub, next)) {
+            tile_wait(nk2);
+            if (ok) scores(sub, nk2);
+          }
         }
         if (!ok) break;
         fixed += partly;
-        tc::commit(empty + nv % T::ST);
-        if (i + 1 < ke) tc::commit(empty + nk2 % T::ST);
+        tc::commit(empty + slot_of(nv));
+        if (next < ke) tc::commit(empty + slot_of(nk2));
       }
       if (!ok) {  // products in flight end before the tensor memory is freed
         tc::commit(drained);
@@ -367,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       // the product's thread says when the tile is there (a wait on the tile's own barrier
       // could mistake an earlier round of the ring for this one)
       if (!tc::wait_warp(v_check, checked++ & 1, &gave_up)) break;
-      uint8_t* v = ring + (2 * (i - kb) + 1) % T::ST * T::kTileBytes;
+      uint8_t* v = ring + slot_of(2 * (i - kb) + 1) * T::kTileBytes;
       constexpr int kLanes = D / 8, kRowsAtOnce = kFixWarps * 32 / kLanes;
       const int t64 = threadIdx.x - kFixWarp * 32, ch = t64 % kLanes;
       const int from = max(least - i * kTile, 0) / kRowsAtOnce * kRowsAtOnce;
@@ -393,10 +409,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   } else {
     tc::regs_more<208>();
     const int sub = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const int row = it.row0 + sub * kTile + r;
+    const int base = alternate ? 0 : sub * kTile;  // of the item's rows
+    const int row = it.row0 + base + r;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_addr = lane_addr + sub * kTile, o_addr = lane_addr + T::kO + sub * D;
-    if (sub < subs && kb < (sub == 0 ? n_sub[0] : n_sub[1])) {
+    const int n_mine = sub == 0 ? n_sub[0] : n_sub[1];
+    if (sub < subs && kb < n_mine) {
       // this tile's rows of q, 16 bytes a lane, swizzled; rows that do not exist are zero
       constexpr int kChunks = D / 8, kPass = kTile / kChunks, kBatch = 8;
       const int ch = r % kChunks, r8 = r / kChunks;
@@ -425,16 +443,22 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full + sub);
     }
-    const bool mine = sub * kTile + r < it.rows;
+    const bool mine = base + r < it.rows;
+    const bool any_row = base + quad * 32 < it.rows;  // of the warp's
     const int see = mine ? sees(row) : 0;
-    const int sub_least = sees(it.row0 + sub * kTile);
+    const int sub_least = sees(it.row0 + base);
+    const int step = alternate ? 2 : 1;
     const float c = p.c;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    const int n_mine = sub == 0 ? n_sub[0] : n_sub[1];
-    for (int i = kb; i < n_mine; ++i) {
-      ok = tc::wait_warp(s_full + sub, (i - kb) & 1, &gave_up);
+    int round = 0;
+    for (int i = kb + (alternate ? sub : 0); i < n_mine; i += step, ++round) {
+      ok = tc::wait_warp(s_full + sub, round & 1, &gave_up);
       if (!ok) break;
+      if (!any_row) {  // rows that do not exist: whatever lies in P stays in their sums
+        if (lane == 0) mbar_arrive(p_full + sub);
+        continue;
+      }
       tc::fence_after();
       uint32_t s[kTile];
 #pragma unroll
@@ -457,12 +481,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       // the exponentials below need not carry it
       if (!(top < INFINITY)) l = NAN, top = m;
       top = fmaxf(m, top);
-      if (__any_sync(0xffffffffu, top > m + kRaise || (i == kb))) {
+      if (__any_sync(0xffffffffu, top > m + kRaise || round == 0)) {
         const float f = top == m ? 1.f : exp2_approx(m - top);
         m = top;
         l *= f;
-        if (i > kb) {
-          ok = tc::wait_warp(o_done + sub, (i - kb - 1) & 1, &gave_up);
+        if (round > 0) {
+          ok = tc::wait_warp(o_done + sub, (round - 1) & 1, &gave_up);
           if (!ok) break;
           tc::fence_after();
 #pragma unroll
@@ -500,14 +524,32 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       if (lane == 0) mbar_arrive(p_full + sub);
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
-    // the row's m and l stay in registers for the end
-    const int n = n_mine - kb;
-    if (ok && n > 0) ok = tc::wait_warp(o_done + sub, (n - 1) & 1, &gave_up);
+    // `round` key tiles are in the row's m, l and O
+    if (ok && round > 0) ok = tc::wait_warp(o_done + sub, (round - 1) & 1, &gave_up);
     tc::fence_after();
     asm volatile("bar.sync 2, %0;" ::"n"(256 + 32 * kFixWarps) : "memory");  // poison is known
+    float* other_o = reinterpret_cast<float*>(qs);  // [D][128], the products are done with q
+    float2* other_ml = reinterpret_cast<float2*>(qs + 2 * T::kTileBytes);
+    if (alternate) {
+      if (sub == 1) {
+        if (round > 0 && any_row && ok) {
+#pragma unroll 1
+          for (int x = 0; x < D; x += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            tc::tmem_ld32(o_addr + x, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) other_o[(x + y) * kTile + r] = __uint_as_float(o[y]);
+          }
+        }
+        other_ml[r] = make_float2(m, round > 0 ? l : -1.f);
+      }
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+    }
     const bool slow = poison != 0;
     const int tok = it.q0 + row / g, h = kh * g + row % g;
-    if (sub < subs && ok) {
+    if (sub < subs && ok && any_row) {
       if (slow) {
 #pragma unroll 1
         for (int x = 0; x < 32; ++x) {
@@ -518,16 +560,33 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         }
       } else {
         const RowOut dst = row_out(p, D, split, tok, h);
+        float f0 = 1.f, f1 = 0.f;  // this tile's share and the other's
+        if (alternate) {
+          const float2 ml = other_ml[r];
+          if (ml.y != -1.f) {
+            const float both = fmaxf(m, ml.x);
+            f0 = m == both ? 1.f : exp2_approx(m - both);
+            f1 = ml.x == both ? 1.f : exp2_approx(ml.x - both);
+            m = both;
+            l = fmaf(ml.y, f1, l * f0);
+          }
+        }
+        const bool joined = alternate && n_mine - kb > 1;
         const float inv = see > 0 ? 1.f / l : 0.f;
 #pragma unroll
         for (int x = 0; x < D; x += 32) {
           uint32_t o[32];
-          if (n > 0) {
+          if (round > 0) {
             __syncwarp();
             tc::tmem_ld32(o_addr + x, o);
             tc::wait_ld();
           }
-          if (n <= 0 || see == 0)
+          if (joined)
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              o[y] = __float_as_uint(fmaf(other_o[(x + y) * kTile + r], f1,
+                                          __uint_as_float(o[y]) * f0));
+          if (round == 0 || see == 0)
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = 0;
           if (mine && p.splits == 1) {

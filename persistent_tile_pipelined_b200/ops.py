@@ -20,6 +20,9 @@ from .synth import mxfp4_pitch
 _TYPES = {torch.bfloat16: tre.TRE_BF16, torch.float32: tre.TRE_F32}
 
 
+# torch.cuda.current_stream(d).cuda_stream without the Stream object (3 us of a 10 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _SMS = {}  # device index -> SM count
 
 
@@ -67,7 +70,7 @@ def _ptr(t) -> Optional[int]:
 
 def _call(fn, device, *args) -> None:
     """fn(*args, current stream) with `device` current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _raw_stream(device.index)
     if device.index == torch.cuda.current_device():
         status = fn(*args, stream)
     else:
