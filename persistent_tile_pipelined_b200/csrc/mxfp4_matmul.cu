@@ -112,11 +112,17 @@ __device__ __forceinline__ void put(Out* p, float v) {
   else *p = __float2bfloat16_rn(v);
 }
 
+// Rows of x per copy: a tile brings only the boxes that hold rows of its expert (what the
+// product makes of the rest of its N side is not stored).
+template <int N>
+constexpr int kBoxOf = N > 64 ? 64 : 16;
+
 template <int N, class Out>
 __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap xmap,
                         const __grid_constant__ CUtensorMap wmap, const MatmulParams p) {
   using T = Tile<N>;
+  constexpr int kBox = kBoxOf<N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -199,15 +205,18 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
   if (warp == kCopyWarp) {
     if (tc::elect_one()) {
       int it = 0;
+      const int boxes = (nt + kBox - 1) / kBox;  // rows of x that the expert has, by the box
       for (; it < stages; ++it) {
         const int slot = it % T::ST;
         if (!tc::wait(empty + slot, (it / T::ST & 1) ^ 1, &gave_up)) break;
         uint8_t* x = ring + slot * T::kStage;
         const int k0 = (s0 + it) * T::KS;
-        mbar_arrive_expect_tx(full + slot, T::kStage);
+        mbar_arrive_expect_tx(full + slot, boxes * kBox * T::KS * 2 + T::kWBytes);
 #pragma unroll
         for (int h = 0; h < T::KS / 64; ++h)
-          tc::load_2d(x + h * N * 128, &xmap, k0 + h * 64, t0, full + slot);
+          for (int b = 0; b < boxes; ++b)
+            tc::load_2d(x + h * N * 128 + b * kBox * 128, &xmap, k0 + h * 64, t0 + b * kBox,
+                        full + slot);
         tc::load_2d(x + T::kXBytes, &wmap, k0 / 2, expert * p.n + r0, full + slot);
       }
       if (gave_up)  // copies in flight land before the CTA ends
@@ -217,7 +226,7 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
     }
   } else if (warp == kMmaWarp) {
     if (tc::elect_one()) {
-      constexpr uint32_t idesc = tc::idesc_bf16(kRows, N, 0);
+      const uint32_t idesc = tc::idesc_bf16(kRows, min(N, (nt + 15) & ~15), 0);
       bool ok = true;
       for (int it = 0; it < stages && ok; ++it) {
         const int slot = it % T::ST, buf = it % T::kABufs;
@@ -415,7 +424,7 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
   CUtensorMap xmap, wmap;
   const uint64_t xd[2] = {(uint64_t)k, (uint64_t)rows};
   const uint64_t xs[1] = {(uint64_t)(rows == 1 ? k : x_row_stride) * 2};
-  const uint32_t xb[2] = {64, (uint32_t)tile};
+  const uint32_t xb[2] = {64, tile > 64 ? 64u : 16u};  // kBoxOf
   st = encode_map(op, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xs, xb,
                   CU_TENSOR_MAP_SWIZZLE_128B, &xmap);
   if (st != TRE_OK) return st;

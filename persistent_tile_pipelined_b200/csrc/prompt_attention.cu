@@ -194,6 +194,87 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, int split, int tok
   }
 }
 
+// The barriers behind the tiles in shared memory: `full` and, ST + 1 further, `empty` of the
+// ring's places, then these.
+enum { kBarQ = 0, kBarS = 2, kBarP = 4, kBarO = 6, kBarFixed = 8, kBarCheck = 9, kBarDrained = 10 };
+
+// The matrix products of key tiles [kb, ke) by one thread; n0, n1: the row tiles' key tiles.
+// kAlternate: key tile i belongs to row tile (i - kb) mod 2, whose S runs two key tiles ahead of
+// its O; else both row tiles take every key tile, S one ahead.
+template <int D, bool kAlternate>
+__device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint64_t* bars,
+                                               uint32_t tmem, int kb, int ke, int n0, int n1,
+                                               int least, volatile int* gave_up) {
+  using T = Shape<D>;
+  constexpr uint32_t id_s = tc::idesc_bf16(kTile, kTile, 0);
+  constexpr uint32_t id_o = tc::idesc_bf16(kTile, D, 1);
+  constexpr int kPlaces = kAlternate ? T::ST + 1 : T::ST, kAhead = kAlternate ? 2 : 1;
+  uint64_t* empty = full + T::ST + 1;
+  const uint32_t ring = smem_u32(qs + (kAlternate ? 1 : 2) * T::kTileBytes);
+  const int total = ke - kb;
+  const int count[2] = {n0 - kb, n1 - kb};
+  auto takes = [&](int sub, int i) {
+    return i < count[sub] && (!kAlternate || (i & 1) == sub);
+  };
+  auto arrived = [&](int n) {
+    return tc::wait(full + n % kPlaces, n / kPlaces & 1, gave_up);
+  };
+  auto scores = [&](int sub, int n) {
+    const uint32_t q = smem_u32(qs) + (kAlternate ? 0 : sub * T::kTileBytes);
+    const uint32_t k = ring + n % kPlaces * T::kTileBytes;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const uint32_t at = (j / 4) * kTile * 128 + (j % 4) * 32;
+      tc::mma_ss(tmem + sub * kTile, tc::smem_desc(q + at, 16, 1024),
+                 tc::smem_desc(k + at, 16, 1024), id_s, j > 0);
+    }
+    tc::commit(bars + kBarS + sub);
+  };
+  auto outputs = [&](int sub, int n, bool add) {
+    const uint32_t v = ring + n % kPlaces * T::kTileBytes;
+#pragma unroll
+    for (int j = 0; j < kTile / 16; ++j)
+      tc::mma_ts(tmem + T::kO + sub * D, tmem + sub * kTile + j * 8,
+                 tc::smem_desc(v + j * 2048, kTile * 128, 1024), id_o, add || j > 0);
+    tc::commit(bars + kBarO + sub);
+  };
+  for (int i = 0; i < min(kAhead, total); ++i) {
+    if (!arrived(2 * i)) return false;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      if (!takes(sub, i)) continue;
+      if (!tc::wait(bars + kBarQ + (kAlternate ? 0 : sub), 0, gave_up)) return false;
+      tc::fence_after();
+      scores(sub, 2 * i);
+    }
+    tc::commit(empty + 2 * i % kPlaces);
+  }
+  int fixed = 0;
+  for (int i = 0; i < total; ++i) {
+    const int nv = 2 * i + 1, next = i + kAhead, nk = 2 * next;
+    if (!arrived(nv)) return false;
+    const bool partly = (kb + i + 1) * kTile > least;
+    if (partly) mbar_arrive(bars + kBarCheck);
+    const int round = kAlternate ? i >> 1 : i;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      if (!takes(sub, i)) continue;
+      if (!tc::wait(bars + kBarP + sub, round & 1, gave_up)) return false;
+      if (partly && !tc::wait(bars + kBarFixed, fixed & 1, gave_up)) return false;
+      tc::fence_after();
+      outputs(sub, nv, round > 0);
+      if (takes(sub, next)) {
+        if (!arrived(nk)) return false;
+        scores(sub, nk);
+      }
+    }
+    fixed += partly;
+    tc::commit(empty + nv % kPlaces);
+    if (next < total) tc::commit(empty + nk % kPlaces);
+  }
+  return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsAttn, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -205,12 +286,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(qs + (2 + T::ST) * T::kTileBytes);
   uint64_t* empty = full + T::ST + 1;
   uint64_t* q_full = empty + T::ST + 1;
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
-  uint64_t* v_fixed = o_done + 2;
-  uint64_t* v_check = v_fixed + 1;
-  uint64_t* drained = v_check + 1;
+  uint64_t* s_full = q_full + kBarS;
+  uint64_t* p_full = q_full + kBarP;
+  uint64_t* o_done = q_full + kBarO;
+  uint64_t* v_fixed = q_full + kBarFixed;
+  uint64_t* v_check = q_full + kBarCheck;
+  uint64_t* drained = q_full + kBarDrained;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up, poison;
   __shared__ Item item;
@@ -272,102 +353,37 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   n_sub[1] = alternate ? n_sub[0] : min(n_sub[1], ke);
 
   uint8_t* ring = qs + (alternate ? 1 : 2) * T::kTileBytes;
-  // the n-th copy's place and how often that was used before: K and V tiles in turn
-  auto slot_of = [&](int n) { return alternate ? n % (T::ST + 1) : n % T::ST; };
-  auto round_of = [&](int n) { return alternate ? n / (T::ST + 1) : n / T::ST; };
+  // places of the ring: K and V tiles take them in turn
+  const int places = alternate ? T::ST + 1 : T::ST;
 
   // Registers: 384 threads x 168 at launch; the softmax warps hold a row of scores (256 x 208)
   // and the others give theirs up (128 x 80).
   if (warp >= kCopyWarp) tc::regs_less<80>();
   if (warp == kCopyWarp) {
     if (tc::elect_one()) {
-      int n = 0;
+      int n = 0, slot = 0, phase = 0;
       const int total = 2 * (ke - kb);
       for (; n < total; ++n) {
-        const int slot = slot_of(n);
-        if (!tc::wait(empty + slot, (round_of(n) & 1) ^ 1, &gave_up)) break;
+        if (!tc::wait(empty + slot, phase ^ 1, &gave_up)) break;
         uint8_t* dst = ring + slot * T::kTileBytes;
         mbar_arrive_expect_tx(full + slot, T::kTileBytes);
         const int row = it.k0 + (kb + n / 2) * kTile;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
           tc::load_3d(dst + h * kTile * 128, n & 1 ? &vmap : &kmap, h * 64, row, kh, full + slot);
+        if (++slot == places) slot = 0, phase ^= 1;
       }
       if (gave_up)  // copies in flight land before the CTA ends
-        for (int i = max(0, n - T::ST - 1); i < n; ++i)
-          for (int x = 0; x < 100000 && !mbar_try_wait(full + slot_of(i), round_of(i) & 1); ++x) {
+        for (int i = max(0, n - places); i < n; ++i)
+          for (int x = 0; x < 100000 && !mbar_try_wait(full + i % places, i / places & 1); ++x) {
           }
     }
   } else if (warp == kMmaWarp) {
     if (tc::elect_one()) {
-      constexpr uint32_t id_s = tc::idesc_bf16(kTile, kTile, 0);
-      constexpr uint32_t id_o = tc::idesc_bf16(kTile, D, 1);
-      bool ok = true;
-      auto tile_wait = [&](int n) {
-        ok = ok && tc::wait(full + slot_of(n), round_of(n) & 1, &gave_up);
-      };
-      auto scores = [&](int sub, int n) {
-        const uint32_t q = smem_u32(qs + (alternate ? 0 : sub * T::kTileBytes));
-        const uint32_t k = smem_u32(ring + slot_of(n) * T::kTileBytes);
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t at = (j / 4) * kTile * 128 + (j % 4) * 32;
-          tc::mma_ss(tmem + sub * kTile, tc::smem_desc(q + at, 16, 1024),
-                     tc::smem_desc(k + at, 16, 1024), id_s, j > 0);
-        }
-        tc::commit(s_full + sub);
-      };
-      auto outputs = [&](int sub, int n, bool add) {
-        const uint32_t v = smem_u32(ring + slot_of(n) * T::kTileBytes);
-#pragma unroll
-        for (int j = 0; j < kTile / 16; ++j)
-          tc::mma_ts(tmem + T::kO + sub * D, tmem + sub * kTile + j * 8,
-                     tc::smem_desc(v + j * 2048, kTile * 128, 1024), id_o, add || j > 0);
-        tc::commit(o_done + sub);
-      };
-      // alternating: tile i of the keys belongs to row tile (i - kb) mod 2, whose S follows two
-      // key tiles ahead of its O; else both row tiles take every key tile, S one ahead
-      const int ahead = alternate ? 2 : 1;
-      auto takes = [&](int sub, int i) {
-        return i < n_sub[sub] && (!alternate || ((i - kb) & 1) == sub);
-      };
-      for (int i = kb; i < min(kb + ahead, ke) && ok; ++i) {
-        tile_wait(2 * (i - kb));
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          if (!ok || !takes(sub, i)) continue;
-          if (i == kb || alternate) ok = tc::wait(q_full + (alternate ? 0 : sub), 0, &gave_up);
-          if (!ok) continue;
-          tc::fence_after();
-          scores(sub, 2 * (i - kb));
-        }
-        tc::commit(empty + slot_of(2 * (i - kb)));
-      }
-      int fixed = 0;
-      for (int i = kb; i < ke && ok; ++i) {
-        const int nv = 2 * (i - kb) + 1, next = i + ahead, nk2 = 2 * (next - kb);
-        tile_wait(nv);
-        const bool partly = (i + 1) * kTile > least;
-        if (partly && ok) mbar_arrive(v_check);
-        const int round = alternate ? (i - kb) >> 1 : i - kb;
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          if (!takes(sub, i) || !ok) continue;
-          ok = tc::wait(p_full + sub, round & 1, &gave_up) &&
-               (!partly || tc::wait(v_fixed, fixed & 1, &gave_up));
-          if (!ok) continue;
-          tc::fence_after();
-          outputs(sub, nv, round > 0);
-          if (takes(sub, next)) {
-            tile_wait(nk2);
-            if (ok) scores(sub, nk2);
-          }
-        }
-        if (!ok) break;
-        fixed += partly;
-        tc::commit(empty + slot_of(nv));
-        if (next < ke) tc::commit(empty + slot_of(nk2));
-      }
+      const bool ok = alternate ? issue_products<D, true>(qs, full, q_full, tmem, kb, ke, n_sub[0],
+                                                          n_sub[1], least, &gave_up)
+                                : issue_products<D, false>(qs, full, q_full, tmem, kb, ke,
+                                                           n_sub[0], n_sub[1], least, &gave_up);
       if (!ok) {  // products in flight end before the tensor memory is freed
         tc::commit(drained);
         for (int x = 0; x < 100000 && !mbar_try_wait(drained, 0); ++x) {
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       // the product's thread says when the tile is there (a wait on the tile's own barrier
       // could mistake an earlier round of the ring for this one)
       if (!tc::wait_warp(v_check, checked++ & 1, &gave_up)) break;
-      uint8_t* v = ring + slot_of(2 * (i - kb) + 1) * T::kTileBytes;
+      uint8_t* v = ring + (2 * (i - kb) + 1) % places * T::kTileBytes;
       constexpr int kLanes = D / 8, kRowsAtOnce = kFixWarps * 32 / kLanes;
       const int t64 = threadIdx.x - kFixWarp * 32, ch = t64 % kLanes;
       const int from = max(least - i * kTile, 0) / kRowsAtOnce * kRowsAtOnce;
