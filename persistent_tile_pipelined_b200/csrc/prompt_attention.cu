@@ -196,7 +196,16 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, int split, int tok
 
 // The barriers behind the tiles in shared memory: `full` and, ST + 1 further, `empty` of the
 // ring's places, then these.
-enum { kBarQ = 0, kBarS = 2, kBarP = 4, kBarO = 6, kBarFixed = 8, kBarCheck = 9, kBarDrained = 10 };
+enum {
+  kBarQ = 0,
+  kBarS = 2,
+  kBarHalf = 4,  // the first half of P is there
+  kBarP = 6,
+  kBarO = 8,
+  kBarFixed = 10,
+  kBarCheck = 11,
+  kBarDrained = 12
+};
 
 // The matrix products of key tiles [kb, ke) by one thread; n0, n1: the row tiles' key tiles.
 // kAlternate: key tile i belongs to row tile (i - kb) mod 2, whose S runs two key tiles ahead of
@@ -230,13 +239,13 @@ __device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint
     }
     tc::commit(bars + kBarS + sub);
   };
-  auto outputs = [&](int sub, int n, bool add) {
+  auto outputs = [&](int sub, int n, bool add, int half) {
     const uint32_t v = ring + n % kPlaces * T::kTileBytes;
 #pragma unroll
-    for (int j = 0; j < kTile / 16; ++j)
+    for (int j = half * kTile / 32; j < (half + 1) * kTile / 32; ++j)
       tc::mma_ts(tmem + T::kO + sub * D, tmem + sub * kTile + j * 8,
                  tc::smem_desc(v + j * 2048, kTile * 128, 1024), id_o, add || j > 0);
-    tc::commit(bars + kBarO + sub);
+    if (half) tc::commit(bars + kBarO + sub);
   };
   for (int i = 0; i < min(kAhead, total); ++i) {
     if (!arrived(2 * i)) return false;
@@ -259,10 +268,13 @@ __device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       if (!takes(sub, i)) continue;
-      if (!tc::wait(bars + kBarP + sub, round & 1, gave_up)) return false;
+      if (!tc::wait(bars + kBarHalf + sub, round & 1, gave_up)) return false;
       if (partly && !tc::wait(bars + kBarFixed, fixed & 1, gave_up)) return false;
       tc::fence_after();
-      outputs(sub, nv, round > 0);
+      outputs(sub, nv, round > 0, 0);
+      if (!tc::wait(bars + kBarP + sub, round & 1, gave_up)) return false;
+      tc::fence_after();
+      outputs(sub, nv, true, 1);
       if (takes(sub, next)) {
         if (!arrived(nk)) return false;
         scores(sub, nk);
@@ -287,6 +299,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   uint64_t* empty = full + T::ST + 1;
   uint64_t* q_full = empty + T::ST + 1;
   uint64_t* s_full = q_full + kBarS;
+  uint64_t* p_half = q_full + kBarHalf;
   uint64_t* p_full = q_full + kBarP;
   uint64_t* o_done = q_full + kBarO;
   uint64_t* v_fixed = q_full + kBarFixed;
@@ -315,6 +328,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 4);
       mbar_init(s_full + i, 1);
+      mbar_init(p_half + i, 4);
       mbar_init(p_full + i, 4);
       mbar_init(o_done + i, 1);
     }
@@ -472,7 +486,10 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       ok = tc::wait_warp(s_full + sub, round & 1, &gave_up);
       if (!ok) break;
       if (!any_row) {  // rows that do not exist: whatever lies in P stays in their sums
-        if (lane == 0) mbar_arrive(p_full + sub);
+        if (lane == 0) {
+          mbar_arrive(p_half + sub);
+          mbar_arrive(p_full + sub);
+        }
         continue;
       }
       tc::fence_after();
@@ -533,11 +550,11 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
           pk[y] = pack_bf16(e.x, e.y);
         }
         tc::tmem_st32(s_addr + x / 2, pk);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive((x == 0 ? p_half : p_full) + sub);
       }
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + sub);
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     // `round` key tiles are in the row's m, l and O
