@@ -24,18 +24,20 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9, kThreadsMm = 320;  // warps 0-7: two 
 
 template <int N>
 struct Tile {
-  static constexpr int KS = N >= 128 ? 64 : 128;     // weights per stage
-  static constexpr int ST = N == 256 ? 6 : N == 128 ? 5 : N == 64 ? 4 : N == 32 ? 6 : 8;
-  static constexpr int kABufs = N == 256 ? 8 : N == 128 ? 4 : 3;
-  static constexpr int kACols = KS / 2;              // tensor-memory columns of one A stage
+  static constexpr int KW = 256;                     // weights of a row per copy: 128 bytes
+  static constexpr int KS = N >= 128 ? 64 : 128;     // weights per step: decode, product
+  static constexpr int kSteps = KW / KS;             // steps per copy of weights
+  static constexpr int WST = N == 256 ? 3 : N == 128 ? 2 : N == 64 ? 3 : N == 32 ? 4 : 5;
+  static constexpr int XST = N == 256 ? 5 : N == 64 ? 3 : 4;
+  static constexpr int kABufs = N == 256 ? 8 : N == 128 ? 4 : 2;  // an equal number per warpgroup
+  static constexpr int kACols = KS / 2;              // tensor-memory columns of one A step
   static constexpr int kCols = N == 256 ? 512 : 256;
   static constexpr int kDCol = kABufs * kACols;
-  static constexpr int kXBytes = N * KS * 2, kWBytes = kRows * KS / 2;
-  static constexpr int kStage = kXBytes + kWBytes;
-  static constexpr int kSmem = ST * kStage + 1024 + 256;
+  static constexpr int kXBytes = N * KS * 2, kWBytes = kRows * KW / 2;
+  static constexpr int kSmem = WST * kWBytes + XST * kXBytes + 1024 + 512;
   static constexpr int kCtas = N == 256 ? 1 : 2;     // per SM
   static_assert(kDCol + N <= kCols, "tensor memory");
-  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory");
 };
 
 struct MatmulParams {
@@ -44,6 +46,7 @@ struct MatmulParams {
   void* out;
   int64_t out_stride, pitch;
   int32_t rows, n, k, n_experts, splits;
+  uint32_t four;  // 4 (see e2m1x8)
   int32_t* status;
 };
 
@@ -52,13 +55,15 @@ struct MatmulParams {
 // mantissa bits, which is the number times 2^-126 (its subnormal 0.5 included).  A byte
 // permute doubles the nibble's byte into both bytes of its half, once shifted so that both
 // nibbles stand high: the sign is then in place and the magnitude two bits below its own.
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t* o) {
+// `four` is 4, but not a constant: the shift by two is then an integer multiply-add, off the
+// logic unit, which is what bounds the decoding.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t four, uint32_t* o) {
   const uint32_t w4 = w << 4;
   constexpr uint32_t sel[4] = {0x4400, 0x5511, 0x6622, 0x7733};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t p = __byte_perm(w4, w, sel[i]);
-    o[i] = (p & 0x80008000u) | ((p << 2) & 0x01c001c0u);
+    o[i] = (p & 0x00700070u) * four + (p & 0x80008000u);
   }
 }
 
@@ -68,23 +73,53 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// 32 codes times their scale 2^(s - 127) as 16 bf16 pairs.  The pattern's 2^-126 and the
-// scale make one exact factor 2^(s - 1), representable up to s = 128; larger scales (and NaN,
-// 255) multiply once more.
-__device__ __forceinline__ void decode32(const uint4 c, uint32_t s, uint32_t* o) {
+// 32 codes times their scale 2^(s - 127) as 16 bf16 pairs, s the byte `at` of `word`.  The
+// pattern's 2^-126 and the scale make one exact factor 2^(s - 1), representable up to s = 128;
+// larger scales (and NaN, 255) multiply once more (kBig: there may be such).
+template <bool kBig>
+__device__ __forceinline__ void decode32(const uint4 c, uint32_t word, int at, uint32_t four,
+                                         uint32_t* o) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  const uint32_t f = (min(s, 128u) + 126u) << 7;
-  const uint32_t f2 = f | f << 16;
+  const uint32_t s2 = __byte_perm(word, 0, 0x4040 + 0x0101 * at);  // s in both halves
+  const uint32_t s = s2 & 0xffffu;
+  uint32_t f2 = s2 * 128u + (126u << 7 | 126u << 23);
+  if (kBig && s > 128u) f2 = 0x7f007f00u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) e2m1x8(w[j], o + 4 * j);
+  for (int j = 0; j < 4; ++j) e2m1x8(w[j], four, o + 4 * j);
 #pragma unroll
   for (int j = 0; j < 16; ++j) o[j] = mul_bf16x2(o[j], f2);
-  if (s > 128u) {
+  if (kBig && s > 128u) {
     const uint32_t h = s == 255u ? 0x7fc0u : (s - 1u) << 7;
     const uint32_t h2 = h | h << 16;
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j] = mul_bf16x2(o[j], h2);
   }
+}
+
+// A step's codes (16-byte chunks q) into tensor memory, 32 columns (64 weights) at a time: the
+// first half is decoded before the place is waited for, the second while the first is stored.
+// By whole warps; false when the wait gave up.
+template <int kChunks, bool kBig>
+__device__ __forceinline__ bool decode_step(const uint4* q, uint32_t word, uint32_t four,
+                                            uint32_t addr, uint64_t* empty, uint32_t parity,
+                                            volatile int* gave_up) {
+#pragma unroll
+  for (int c = 0; c < kChunks; c += 2) {
+    uint32_t v[32];
+    decode32<kBig>(q[c], word, c, four, v);
+    decode32<kBig>(q[c + 1], word, c + 1, four, v + 16);
+    if (c == 0) {
+      if (!tc::wait_warp(empty, parity, gave_up)) return false;
+      tc::fence_after();
+    }
+    tc::tmem_st32(addr + c * 16, v);
+  }
+  return true;
+}
+
+// Whether any of 4 bytes exceeds 128.
+__device__ __forceinline__ uint32_t over128(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) & w & 0x80808080u;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -126,9 +161,12 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + T::ST * T::kStage);
-  uint64_t* empty = full + T::ST;
-  uint64_t* a_full = empty + T::ST;
+  uint8_t* xring = ring + T::WST * T::kWBytes;
+  uint64_t* w_full = reinterpret_cast<uint64_t*>(xring + T::XST * T::kXBytes);
+  uint64_t* w_empty = w_full + T::WST;
+  uint64_t* x_full = w_empty + T::WST;
+  uint64_t* x_empty = x_full + T::XST;
+  uint64_t* a_full = x_empty + T::XST;
   uint64_t* a_empty = a_full + T::kABufs;
   uint64_t* done = a_empty + T::kABufs;
   __shared__ uint32_t tmem_base;
@@ -143,30 +181,50 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
       row = y * N;
       count = p.rows - row;
     } else {
-      for (int e0 = 0; e0 < p.n_experts && found < 0; e0 += 32) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < p.n_experts) {
+      // a lane takes `per` experts in a row; their counts load together
+      const int per = (p.n_experts + 31) / 32, first = lane * per;
+      auto bounds = [&](int e, int& lo, int& hi) {
+        lo = hi = 0;
+        if (e < p.n_experts && e < first + per) {
           lo = min(max(p.offsets[e], 0), p.rows);
-          hi = min(max(p.offsets[e + 1], 0), p.rows);
+          hi = max(min(max(p.offsets[e + 1], 0), p.rows), lo);
         }
-        const int tiles = hi > lo ? (hi - lo + N - 1) / N : 0;
-        int sum = tiles;  // inclusive over the lanes
+      };
+      int tiles = 0;
+      for (int e = first; e < first + per; e += 8) {
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, sum, d);
-          if (lane >= d) sum += up;
+        for (int i = 0; i < 8; ++i) {
+          int lo, hi;
+          bounds(e + i, lo, hi);
+          tiles += (hi - lo + N - 1) / N;
         }
-        const uint32_t mine = __ballot_sync(0xffffffffu, sum > y);
-        if (mine) {
-          const int l = __ffs(mine) - 1;
-          const int before = __shfl_sync(0xffffffffu, sum - tiles, l);
-          found = e0 + l;
-          row = __shfl_sync(0xffffffffu, lo, l) + (y - before) * N;
-          count = __shfl_sync(0xffffffffu, hi, l) - row;
-        } else {
-          y -= __shfl_sync(0xffffffffu, sum, 31);
+      }
+      int sum = tiles;  // inclusive over the lanes
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      const uint32_t mine = __ballot_sync(0xffffffffu, sum > y);
+      if (mine) {
+        const int l = __ffs(mine) - 1;
+        if (lane == l) {
+          y -= sum - tiles;
+          for (int e = first; found < 0; ++e) {
+            int lo, hi;
+            bounds(e, lo, hi);
+            const int t = (hi - lo + N - 1) / N;
+            if (y < t) {
+              found = e;
+              row = lo + y * N;
+              count = hi - row;
+            }
+            y -= t;
+          }
         }
+        found = __shfl_sync(0xffffffffu, found, l);
+        row = __shfl_sync(0xffffffffu, row, l);
+        count = __shfl_sync(0xffffffffu, count, l);
       }
     }
     if (lane == 0) {
@@ -176,9 +234,13 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
       gave_up = 0;
     }
   } else if (warp == 1 && lane == 0) {
-    for (int i = 0; i < T::ST; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+    for (int i = 0; i < T::WST; ++i) {
+      mbar_init(w_full + i, 1);
+      mbar_init(w_empty + i, 8);  // a lane of each decode warp
+    }
+    for (int i = 0; i < T::XST; ++i) {
+      mbar_init(x_full + i, 1);
+      mbar_init(x_empty + i, 1);
     }
     for (int i = 0; i < T::kABufs; ++i) {
       mbar_init(a_full + i, 4);
@@ -186,6 +248,9 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
     }
     mbar_init(done, 1);
     fence_mbar_init();
+  } else if (warp == kCopyWarp && lane == 0) {
+    tc::prefetch_map(&wmap);
+    tc::prefetch_map(&xmap);
   }
   __syncthreads();
   const int expert = tile[0], t0 = tile[1], nt = tile[2];
@@ -198,49 +263,77 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
 
   const int split = p.splits > 1 ? (int)cluster_rank() : 0;
   const int r0 = (int)(blockIdx.x / p.splits) * kRows;
-  const int all = (p.k + T::KS - 1) / T::KS;
-  const int s0 = (int)((int64_t)all * split / p.splits);
-  const int stages = (int)((int64_t)all * (split + 1) / p.splits) - s0;
+  // whole groups of 512 weights (16 scale bytes) per part of a split
+  const int groups = (p.k + 511) / 512;
+  const int k_begin = (int)((int64_t)groups * split / p.splits) * 512;
+  const int k_end = min((int)((int64_t)groups * (split + 1) / p.splits) * 512, p.k);
+  const int stages = (max(k_end - k_begin, 0) + T::KS - 1) / T::KS;
 
   if (warp == kCopyWarp) {
     if (tc::elect_one()) {
-      int it = 0;
+      int it = 0, w = 0;
       const int boxes = (nt + kBox - 1) / kBox;  // rows of x that the expert has, by the box
-      for (; it < stages; ++it) {
-        const int slot = it % T::ST;
-        if (!tc::wait(empty + slot, (it / T::ST & 1) ^ 1, &gave_up)) break;
-        uint8_t* x = ring + slot * T::kStage;
-        const int k0 = (s0 + it) * T::KS;
-        mbar_arrive_expect_tx(full + slot, boxes * kBox * T::KS * 2 + T::kWBytes);
+      const int copies = (stages + T::kSteps - 1) / T::kSteps;
+      long long since = clock64();  // the last copy
+      while (it < stages) {  // whichever ring has a free place
+        bool idle = true;
+        if (w < copies && mbar_test_wait(w_empty + w % T::WST, (w / T::WST & 1) ^ 1)) {
+          const int slot = w % T::WST;
+          mbar_arrive_expect_tx(w_full + slot, T::kWBytes);
+          tc::load_2d(ring + slot * T::kWBytes, &wmap, k_begin / 2 + w * (T::KW / 2),
+                      expert * p.n + r0, w_full + slot);
+          ++w;
+          idle = false;
+        }
+        if (it / T::kSteps < w && mbar_test_wait(x_empty + it % T::XST, (it / T::XST & 1) ^ 1)) {
+          const int slot = it % T::XST;
+          uint8_t* x = xring + slot * T::kXBytes;
+          const int k0 = k_begin + it * T::KS;
+          mbar_arrive_expect_tx(x_full + slot, boxes * kBox * T::KS * 2);
 #pragma unroll
-        for (int h = 0; h < T::KS / 64; ++h)
-          for (int b = 0; b < boxes; ++b)
-            tc::load_2d(x + h * N * 128 + b * kBox * 128, &xmap, k0 + h * 64, t0 + b * kBox,
-                        full + slot);
-        tc::load_2d(x + T::kXBytes, &wmap, k0 / 2, expert * p.n + r0, full + slot);
-      }
-      if (gave_up)  // copies in flight land before the CTA ends
-        for (int i = max(0, it - T::ST); i < it; ++i)
-          for (int n = 0; n < 100000 && !mbar_try_wait(full + i % T::ST, i / T::ST & 1); ++n) {
+          for (int h = 0; h < T::KS / 64; ++h)
+            for (int b = 0; b < boxes; ++b)
+              tc::load_2d(x + h * N * 128 + b * kBox * 128, &xmap, k0 + h * 64, t0 + b * kBox,
+                          x_full + slot);
+          ++it;
+          idle = false;
+        }
+        if (!idle) {
+          since = clock64();
+        } else {
+          __nanosleep(32);
+          if (*(volatile int*)&gave_up || clock64() - since > tc::kWaitClocks) {
+            gave_up = 1;
+            break;
           }
+        }
+      }
+      if (gave_up) {  // copies in flight land before the CTA ends
+        for (int i = max(0, it - T::XST); i < it; ++i)
+          for (int n = 0; n < 100000 && !mbar_try_wait(x_full + i % T::XST, i / T::XST & 1); ++n) {
+          }
+        for (int i = max(0, w - T::WST); i < w; ++i)
+          for (int n = 0; n < 100000 && !mbar_try_wait(w_full + i % T::WST, i / T::WST & 1); ++n) {
+          }
+      }
     }
   } else if (warp == kMmaWarp) {
     if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(kRows, min(N, (nt + 15) & ~15), 0);
       bool ok = true;
       for (int it = 0; it < stages && ok; ++it) {
-        const int slot = it % T::ST, buf = it % T::kABufs;
-        ok = tc::wait(full + slot, it / T::ST & 1, &gave_up) &&
+        const int slot = it % T::XST, buf = it % T::kABufs;
+        ok = tc::wait(x_full + slot, it / T::XST & 1, &gave_up) &&
              tc::wait(a_full + buf, it / T::kABufs & 1, &gave_up);
         if (!ok) break;
         tc::fence_after();
-        const uint32_t x = smem_u32(ring + slot * T::kStage);
+        const uint32_t x = smem_u32(xring + slot * T::kXBytes);
 #pragma unroll
         for (int j = 0; j < T::KS / 16; ++j) {
           const uint64_t b = tc::smem_desc(x + (j / 4) * N * 128 + (j % 4) * 32, 16, 1024);
           tc::mma_ts(tmem + T::kDCol, tmem + buf * T::kACols + j * 8, b, idesc, it + j > 0);
         }
-        tc::commit(empty + slot);
+        tc::commit(x_empty + slot);
         tc::commit(a_empty + buf);
       }
       tc::commit(done);
@@ -249,58 +342,68 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
         }
     }
   } else {
-    // decode: thread = matrix row r0 + 32 (warp mod 4) + lane, warpgroup = stage parity
+    // decode: thread = matrix row r0 + 32 (warp mod 4) + lane, warpgroup = step parity
     const int wg = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     const int64_t row = (int64_t)expert * p.n + min(r0 + r, p.n - 1);
     const uint8_t* scales = p.w + row * p.pitch + p.k / 2;
     const int blocks = p.k / 32;
-    constexpr int kPer = 512 / T::KS;  // stages per 16 scale bytes
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    int group = -1;
-    uint4 sc = make_uint4(0, 0, 0, 0), next = sc;
-    auto fetch = [&](int g) {  // 16 scales; those behind the row's last are never used
-      return g * 16 < blocks ? *reinterpret_cast<const uint4*>(scales + g * 16)
-                             : make_uint4(0, 0, 0, 0);
+    // 16 scales; zero behind the row's last, where the copies bring zero codes
+    auto fetch = [&](int g) {
+      if (g * 16 >= blocks) return make_uint4(0, 0, 0, 0);
+      uint4 v = *reinterpret_cast<const uint4*>(scales + g * 16);
+      const int left = blocks - g * 16;
+      if (left < 16) {
+        auto keep = [&](int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : ~0u >> (32 - 8 * n); };
+        v.x &= keep(left);
+        v.y &= keep(left - 4);
+        v.z &= keep(left - 8);
+        v.w &= keep(left - 12);
+      }
+      return v;
     };
-    if (stages > 0) next = fetch(s0 / kPer);
-    for (int it = wg; it < stages; it += 2) {
-      const int st = s0 + it;
-      if (st / kPer != group) {
-        // (a warpgroup never skips a group: a group has at least 4 stages)
-        if (group < 0 && st / kPer != s0 / kPer) next = fetch(st / kPer);
-        group = st / kPer;
-        sc = next;
-        next = fetch(group + 1);
-      }
-      const int slot = it % T::ST, buf = it % T::kABufs;
-      if (!tc::wait_warp(full + slot, it / T::ST & 1, &gave_up)) break;
-      const uint8_t* codes = ring + slot * T::kStage + T::kXBytes + r * (T::KS / 2);
-      const int first = (st % kPer) * (T::KS / 32);  // of the group's 16 scales
-      const uint32_t word = first / 4 == 0 ? sc.x : first / 4 == 1 ? sc.y : first / 4 == 2 ? sc.z : sc.w;
-      uint32_t v[T::KS / 2];
+    const uint8_t* my_codes = ring + r * (T::KW / 2);
+    constexpr int kChunks = T::KS / 32;  // 16-byte chunks of a step
+    uint4 sc = fetch(k_begin / 512), next = make_uint4(0, 0, 0, 0);
+    bool ok = true;
+    int slot = 0, phase = 0, mine = 0;  // `mine`: steps that this warpgroup has taken
+#pragma unroll 1
+    for (int first = 0; first < stages && ok; first += T::kSteps) {  // a copy of 256 weights
+      const bool odd = (first / T::kSteps) & 1;
+      if (!odd) next = fetch(k_begin / 512 + first / (2 * T::kSteps) + 1);
+      const uint32_t lo = odd ? sc.z : sc.x, hi = odd ? sc.w : sc.y;  // the copy's 8 scales
+      // the same way for the whole warp: its stores to tensor memory go together
+      const bool big = __any_sync(0xffffffffu, (over128(lo) | over128(hi)) != 0);
+      ok = tc::wait_warp(w_full + slot, phase, &gave_up);
 #pragma unroll
-      for (int c = 0; c < T::KS / 32; ++c) {
-        // 16-byte chunks are swizzled within 128 bytes: by row pair (64-byte rows) or by
-        // groups of four rows (32-byte rows)
-        const int at = T::KS == 128 ? c ^ (r >> 1 & 3) : c ^ (r >> 2 & 1);
-        const uint4 q = *reinterpret_cast<const uint4*>(codes + at * 16);
-        const bool in = st * (T::KS / 32) + c < blocks;  // behind the row's end: zero codes
-        decode32(q, in ? word >> (8 * ((first + c) & 3)) & 0xffu : 0u, v + 16 * c);
-      }
-      if (!tc::wait_warp(a_empty + buf, (it / T::kABufs & 1) ^ 1, &gave_up)) break;
-      tc::fence_after();
+      for (int u = 0; u < T::kSteps / 2; ++u) {
+        const int h = 2 * u + wg;
+        if (!ok || first + h >= stages) continue;
+        uint4 q[kChunks];
 #pragma unroll
-      for (int c = 0; c < T::KS / 64; ++c)
-        tc::tmem_st32(lane_addr + buf * T::kACols + c * 32, v + 32 * c);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(a_full + buf);
+        for (int c = 0; c < kChunks; ++c)  // the 128-byte swizzle: chunk c of row r at c ^ (r mod 8)
+          q[c] = *reinterpret_cast<const uint4*>(my_codes + slot * T::kWBytes +
+                                                 ((h * kChunks + c) ^ (r & 7)) * 16);
+        const uint32_t word = kChunks == 4 ? (wg ? hi : lo) : (u ? hi : lo) >> (16 * wg);
+        const int buf = (2 * mine + wg) % T::kABufs;
+        const uint32_t free = (2 * mine / T::kABufs & 1) ^ 1, at = lane_addr + buf * T::kACols;
+        ok = big ? decode_step<kChunks, true>(q, word, p.four, at, a_empty + buf, free, &gave_up)
+                 : decode_step<kChunks, false>(q, word, p.four, at, a_empty + buf, free, &gave_up);
+        if (!ok) continue;
+        ++mine;
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a_full + buf);
+      }
+      if (lane == 0) mbar_arrive(w_empty + slot);
+      if (++slot == T::WST) slot = 0, phase ^= 1;
+      if (odd) sc = next;
     }
     __syncwarp();
     // the sums: warpgroup = half of the rows of x
-    const bool ok = stages == 0 || tc::wait_warp(done, 0, &gave_up);
+    ok = ok && (stages == 0 || tc::wait_warp(done, 0, &gave_up));
     tc::fence_after();
     Out* out = static_cast<Out*>(p.out);
     float* part = reinterpret_cast<float*>(ring);  // split along k: [N][128], ring is idle
@@ -412,14 +515,15 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
   const int64_t pitch = (k / 2 + k / 32 + 15) / 16 * 16;
   const int sms = device_sms();
   MatmulParams p{static_cast<const uint8_t*>(w), offsets, out, out_row_stride, pitch,
-                 (int32_t)rows, (int32_t)n, (int32_t)k, n_experts, 1, ops_status_ptr()};
+                 (int32_t)rows, (int32_t)n, (int32_t)k, n_experts, 1, 4u, ops_status_ptr()};
   OP_ARG(p.status, op, "the operators' status word is not available");
   const int tile = tile_rows(p, sms);
-  const int ks = tile >= 128 ? 64 : 128;
   if (tile <= 32) {  // few tiles: split k over a cluster until the device is busy
-    const int64_t tiles = (n + kRows - 1) / kRows *
-                          std::max<int64_t>(1, std::min<int64_t>(rows, (rows + tile - 1) / tile));
-    while (p.splits < 8 && tiles * p.splits * 2 <= 2 * sms && k / ks >= 4 * p.splits) p.splits *= 2;
+    const int64_t tiles = (n + kRows - 1) / kRows * ((rows + tile - 1) / tile);
+    const int groups = (int)((k + 511) / 512);
+    const int most = (int)std::min<int64_t>({8, groups, std::max<int64_t>(1, 2 * sms / tiles)});
+    const int each = (groups + most - 1) / most;
+    p.splits = (groups + each - 1) / each;
   }
   CUtensorMap xmap, wmap;
   const uint64_t xd[2] = {(uint64_t)k, (uint64_t)rows};
@@ -430,9 +534,9 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
   if (st != TRE_OK) return st;
   const uint64_t wd[2] = {(uint64_t)k / 2, (uint64_t)n * n_experts};
   const uint64_t ws[1] = {(uint64_t)pitch};
-  const uint32_t wb[2] = {(uint32_t)ks / 2, kRows};
+  const uint32_t wb[2] = {Tile<16>::KW / 2, kRows};
   st = encode_map(op, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, wd, ws, wb,
-                  ks == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, &wmap);
+                  CU_TENSOR_MAP_SWIZZLE_128B, &wmap);
   if (st != TRE_OK) return st;
 #define MM(N)                                                                            \
   case N:                                                                                \

@@ -16,12 +16,26 @@ namespace tc {
 // it then sets the CTA's flag, and the caller leaves its loop for the common teardown.
 constexpr long long kWaitClocks = 4000000000ll;
 
+// A probe that may sleep up to a millisecond before it answers: a spinning warp would take
+// issue slots from the warps that it waits for.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (try_wait_long(bar, parity)) return true;
   const long long t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && (*gave_up || clock64() - t0 > kWaitClocks)) {
+  for (;;) {
+    if (try_wait_long(bar, parity)) return true;
+    if (*gave_up || clock64() - t0 > kWaitClocks) {
       *gave_up = 1;
       return false;
     }
