@@ -32,11 +32,13 @@ struct Tile {
   static constexpr int kABufs = N == 256 ? 8 : N == 128 ? 4 : 2;  // an equal number per warpgroup
   static constexpr int kACols = KS / 2;              // tensor-memory columns of one A step
   static constexpr int kCols = N == 256 ? 512 : 256;
+  static constexpr int kDBufs = N <= 64 ? 2 : 1;     // sums of two jobs
   static constexpr int kDCol = kABufs * kACols;
   static constexpr int kXBytes = N * KS * 2, kWBytes = kRows * KW / 2;
   static constexpr int kSmem = WST * kWBytes + XST * kXBytes + 1024 + 512;
+  static constexpr bool kStay = N == 256;            // a CTA takes job after job
   static constexpr int kCtas = N == 256 ? 1 : 2;     // per SM
-  static_assert(kDCol + N <= kCols, "tensor memory");
+  static_assert(kDCol + kDBufs * N <= kCols, "tensor memory");
   static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory");
 };
 
@@ -152,6 +154,10 @@ __device__ __forceinline__ void put(Out* p, float v) {
 template <int N>
 constexpr int kBoxOf = N > 64 ? 64 : 16;
 
+struct Job {
+  int expert, r0, t0, nt;  // rows r0 .. r0 + 127 of its matrix, rows t0 .. t0 + nt - 1 of x
+};
+
 template <int N, class Out>
 __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap xmap,
@@ -169,69 +175,79 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
   uint64_t* a_full = x_empty + T::XST;
   uint64_t* a_empty = a_full + T::kABufs;
   uint64_t* done = a_empty + T::kABufs;
+  uint64_t* d_free = done + T::kDBufs;
   __shared__ uint32_t tmem_base;
-  __shared__ int gave_up, tile[3];  // expert, first row of x, rows of x
+  __shared__ int gave_up, lane_tiles[32], lane_last[32];
+  __shared__ Job first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // the tile's expert: tiles of kN rows, expert by expert
-  if (warp == 0) {
-    int y = blockIdx.y, found = -1, row = 0, count = 0;
-    if (!p.offsets) {
-      found = 0;
-      row = y * N;
-      count = p.rows - row;
-    } else {
-      // a lane takes `per` experts in a row; their counts load together
-      const int per = (p.n_experts + 31) / 32, first = lane * per;
-      auto bounds = [&](int e, int& lo, int& hi) {
-        lo = hi = 0;
-        if (e < p.n_experts && e < first + per) {
-          lo = min(max(p.offsets[e], 0), p.rows);
-          hi = max(min(max(p.offsets[e + 1], 0), p.rows), lo);
-        }
-      };
-      int tiles = 0;
-      for (int e = first; e < first + per; e += 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          int lo, hi;
-          bounds(e + i, lo, hi);
-          tiles += (hi - lo + N - 1) / N;
-        }
-      }
-      int sum = tiles;  // inclusive over the lanes
+  // Tiles of N rows of x, expert by expert.  A lane counts those of `per` experts in a row
+  // (their bounds load together): lane_tiles, and lane_last = the sum up to and with it.
+  const int per = (p.n_experts + 31) / 32;
+  auto bounds = [&](int e, int first, int& lo, int& hi) {
+    lo = hi = 0;
+    if (e < p.n_experts && e < first + per) {
+      lo = p.offsets ? min(max(p.offsets[e], 0), p.rows) : 0;
+      hi = p.offsets ? max(min(max(p.offsets[e + 1], 0), p.rows), lo) : p.rows;
+    }
+  };
+  // A job is a tile of x times 128 rows of its expert; the CTA (a cluster when k is split)
+  // takes every gridDim-th, neighbours the same x.
+  const int row_tiles = (p.n + kRows - 1) / kRows;
+  const int job_step = gridDim.x / p.splits, first_job = blockIdx.x / p.splits;
+  auto find_job = [&](int job) {  // whole warp
+    int y = job / row_tiles;
+    Job j{0, (job - y * row_tiles) * kRows, 0, 0};
+    const int l = __ffs(__ballot_sync(0xffffffffu, lane_last[lane] > y)) - 1;
+    y -= lane_last[l] - lane_tiles[l];
+    for (int e0 = l * per;; e0 += 32) {  // the lane's experts, 32 at a time
+      int lo, hi;
+      bounds(e0 + lane, l * per, lo, hi);
+      const int t = (hi - lo + N - 1) / N;
+      int sum = t;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += up;
       }
       const uint32_t mine = __ballot_sync(0xffffffffu, sum > y);
-      if (mine) {
-        const int l = __ffs(mine) - 1;
-        if (lane == l) {
-          y -= sum - tiles;
-          for (int e = first; found < 0; ++e) {
-            int lo, hi;
-            bounds(e, lo, hi);
-            const int t = (hi - lo + N - 1) / N;
-            if (y < t) {
-              found = e;
-              row = lo + y * N;
-              count = hi - row;
-            }
-            y -= t;
-          }
-        }
-        found = __shfl_sync(0xffffffffu, found, l);
-        row = __shfl_sync(0xffffffffu, row, l);
-        count = __shfl_sync(0xffffffffu, count, l);
+      const int last = __shfl_sync(0xffffffffu, sum, 31);
+      if (mine || e0 + 32 >= l * per + per) {
+        const int m = mine ? __ffs(mine) - 1 : 0;
+        j.expert = e0 + m;
+        j.t0 = __shfl_sync(0xffffffffu, lo + (y - (sum - t)) * N, m);
+        j.nt = min(__shfl_sync(0xffffffffu, hi, m) - j.t0, N);
+        if (!mine) j.nt = 0;  // the offsets changed under the call: no rows
+        return j;
+      }
+      y -= last;
+    }
+  };
+
+  if (warp == 0) {
+    int tiles = 0;
+    for (int e = lane * per; e < lane * per + per; e += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        int lo, hi;
+        bounds(e + i, lane * per, lo, hi);
+        tiles += (hi - lo + N - 1) / N;
       }
     }
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += up;
+    }
+    lane_tiles[lane] = tiles;
+    lane_last[lane] = sum;
+    __syncwarp();
+    Job j{0, 0, 0, 0};
+    if (first_job < lane_last[31] * row_tiles) j = find_job(first_job);
     if (lane == 0) {
-      tile[0] = found;
-      tile[1] = row;
-      tile[2] = min(count, N);
       gave_up = 0;
+      first = j;
     }
   } else if (warp == 1 && lane == 0) {
     for (int i = 0; i < T::WST; ++i) {
@@ -246,183 +262,222 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
       mbar_init(a_full + i, 4);
       mbar_init(a_empty + i, 1);
     }
-    mbar_init(done, 1);
+    for (int i = 0; i < T::kDBufs; ++i) {
+      mbar_init(done + i, 1);
+      mbar_init(d_free + i, 8);
+    }
     fence_mbar_init();
   } else if (warp == kCopyWarp && lane == 0) {
     tc::prefetch_map(&wmap);
     tc::prefetch_map(&xmap);
+  } else if (warp == kMmaWarp) {
+    tc::tmem_alloc(&tmem_base, T::kCols);
   }
-  __syncthreads();
-  const int expert = tile[0], t0 = tile[1], nt = tile[2];
-  if (expert < 0) return;  // the same for every CTA of the cluster
-  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, T::kCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_base;
 
   const int split = p.splits > 1 ? (int)cluster_rank() : 0;
-  const int r0 = (int)(blockIdx.x / p.splits) * kRows;
   // whole groups of 512 weights (16 scale bytes) per part of a split
   const int groups = (p.k + 511) / 512;
   const int k_begin = (int)((int64_t)groups * split / p.splits) * 512;
   const int k_end = min((int)((int64_t)groups * (split + 1) / p.splits) * 512, p.k);
-  const int stages = (max(k_end - k_begin, 0) + T::KS - 1) / T::KS;
+  const int steps = (k_end - k_begin + T::KS - 1) / T::KS;
+  const int copies = (steps + T::kSteps - 1) / T::kSteps;
 
+  const int jobs = lane_last[31] * row_tiles;
+  Job job{0, 0, 0, 0};  // of the reduction at the end
   if (warp == kCopyWarp) {
-    if (tc::elect_one()) {
-      int it = 0, w = 0;
-      const int boxes = (nt + kBox - 1) / kBox;  // rows of x that the expert has, by the box
-      const int copies = (stages + T::kSteps - 1) / T::kSteps;
+    // (the whole warp, one lane issues: see the products)
+    const bool leader = tc::elect_one();
+    int wslot = 0, wphase = 1, xslot = 0, xphase = 1;  // places and the parity that frees them
+    int w_used = 0, x_used = 0;
+    bool ok = true;
+    for (int n = first_job; n < jobs && ok; n = T::kStay ? n + job_step : jobs) {
+      const Job j = n == first_job ? first : find_job(n);
+      const int boxes = (j.nt + kBox - 1) / kBox;  // rows of x that the expert has, by the box
+      const int wrow = j.expert * p.n + j.r0;
       long long since = clock64();  // the last copy
-      while (it < stages) {  // whichever ring has a free place
+      for (int x = 0, w = 0; x < steps;) {  // whichever ring has a free place
         bool idle = true;
-        if (w < copies && mbar_test_wait(w_empty + w % T::WST, (w / T::WST & 1) ^ 1)) {
-          const int slot = w % T::WST;
-          mbar_arrive_expect_tx(w_full + slot, T::kWBytes);
-          tc::load_2d(ring + slot * T::kWBytes, &wmap, k_begin / 2 + w * (T::KW / 2),
-                      expert * p.n + r0, w_full + slot);
-          ++w;
+        if (w < copies && __all_sync(0xffffffffu, mbar_test_wait(w_empty + wslot, wphase))) {
+          if (leader) {
+            mbar_arrive_expect_tx(w_full + wslot, T::kWBytes);
+            tc::load_2d(ring + wslot * T::kWBytes, &wmap, k_begin / 2 + w * (T::KW / 2), wrow,
+                        w_full + wslot);
+          }
+          if (++wslot == T::WST) wslot = 0, wphase ^= 1;
+          ++w, ++w_used;
           idle = false;
         }
-        if (it / T::kSteps < w && mbar_test_wait(x_empty + it % T::XST, (it / T::XST & 1) ^ 1)) {
-          const int slot = it % T::XST;
-          uint8_t* x = xring + slot * T::kXBytes;
-          const int k0 = k_begin + it * T::KS;
-          mbar_arrive_expect_tx(x_full + slot, boxes * kBox * T::KS * 2);
+        if (x / T::kSteps < w &&
+            __all_sync(0xffffffffu, mbar_test_wait(x_empty + xslot, xphase))) {
+          if (leader) {
+            uint8_t* dst = xring + xslot * T::kXBytes;
+            const int k0 = k_begin + x * T::KS;
+            mbar_arrive_expect_tx(x_full + xslot, boxes * kBox * T::KS * 2);
 #pragma unroll
-          for (int h = 0; h < T::KS / 64; ++h)
-            for (int b = 0; b < boxes; ++b)
-              tc::load_2d(x + h * N * 128 + b * kBox * 128, &xmap, k0 + h * 64, t0 + b * kBox,
-                          x_full + slot);
-          ++it;
+            for (int h = 0; h < T::KS / 64; ++h)
+              for (int b = 0; b < boxes; ++b)
+                tc::load_2d(dst + h * N * 128 + b * kBox * 128, &xmap, k0 + h * 64,
+                            j.t0 + b * kBox, x_full + xslot);
+          }
+          if (++xslot == T::XST) xslot = 0, xphase ^= 1;
+          ++x, ++x_used;
           idle = false;
         }
         if (!idle) {
           since = clock64();
         } else {
           __nanosleep(32);
-          if (*(volatile int*)&gave_up || clock64() - since > tc::kWaitClocks) {
+          if (__any_sync(0xffffffffu, *(volatile int*)&gave_up ||
+                                          clock64() - since > tc::kWaitClocks)) {
             gave_up = 1;
+            ok = false;
             break;
           }
         }
       }
-      if (gave_up) {  // copies in flight land before the CTA ends
-        for (int i = max(0, it - T::XST); i < it; ++i)
-          for (int n = 0; n < 100000 && !mbar_try_wait(x_full + i % T::XST, i / T::XST & 1); ++n) {
-          }
-        for (int i = max(0, w - T::WST); i < w; ++i)
-          for (int n = 0; n < 100000 && !mbar_try_wait(w_full + i % T::WST, i / T::WST & 1); ++n) {
-          }
-      }
+    }
+    if (!ok) {  // copies in flight land before the CTA ends
+      for (int i = max(0, x_used - T::XST); i < x_used; ++i)
+        for (int c = 0; c < 100000 && !mbar_try_wait(x_full + i % T::XST, i / T::XST & 1); ++c) {
+        }
+      for (int i = max(0, w_used - T::WST); i < w_used; ++i)
+        for (int c = 0; c < 100000 && !mbar_try_wait(w_full + i % T::WST, i / T::WST & 1); ++c) {
+        }
     }
   } else if (warp == kMmaWarp) {
-    if (tc::elect_one()) {
-      const uint32_t idesc = tc::idesc_bf16(kRows, min(N, (nt + 15) & ~15), 0);
-      bool ok = true;
-      for (int it = 0; it < stages && ok; ++it) {
-        const int slot = it % T::XST, buf = it % T::kABufs;
-        ok = tc::wait(x_full + slot, it / T::XST & 1, &gave_up) &&
-             tc::wait(a_full + buf, it / T::kABufs & 1, &gave_up);
+    // The whole warp runs the loop, so that what the products take is uniform; one lane issues.
+    const bool leader = tc::elect_one();
+    constexpr uint32_t kHi = tc::desc_hi(1024);
+    const uint32_t lo0 = tc::desc_lo(smem_u32(xring), 16);
+    int xslot = 0, xphase = 0, abuf = 0, aphase = 0, dbuf = 0, dphase = 1;
+    bool ok = true;
+    for (int n = first_job; n < jobs && ok; n = T::kStay ? n + job_step : jobs) {
+      const Job j = n == first_job ? first : find_job(n);
+      const uint32_t idesc = tc::idesc_bf16(kRows, max(min(N, (j.nt + 15) & ~15), 16), 0);
+      ok = tc::wait_warp(d_free + dbuf, dphase, &gave_up);
+      for (int x = 0; x < steps && ok; ++x) {
+        ok = tc::wait_warp(x_full + xslot, xphase, &gave_up) &&
+             tc::wait_warp(a_full + abuf, aphase, &gave_up);
         if (!ok) break;
         tc::fence_after();
-        const uint32_t x = smem_u32(xring + slot * T::kXBytes);
+        const uint32_t lo = lo0 + xslot * (T::kXBytes / 16);
+        const uint32_t at = tmem + abuf * T::kACols;
+        if (leader) {
 #pragma unroll
-        for (int j = 0; j < T::KS / 16; ++j) {
-          const uint64_t b = tc::smem_desc(x + (j / 4) * N * 128 + (j % 4) * 32, 16, 1024);
-          tc::mma_ts(tmem + T::kDCol, tmem + buf * T::kACols + j * 8, b, idesc, it + j > 0);
+          for (int i = 0; i < T::KS / 16; ++i)
+            tc::mma_ts(tmem + T::kDCol + dbuf * N, at + i * 8,
+                       tc::desc_of(lo + (i / 4) * (N * 128 / 16) + (i % 4) * 2, kHi), idesc,
+                       i > 0 || x > 0);
+          tc::commit(x_empty + xslot);
+          tc::commit(a_empty + abuf);
         }
-        tc::commit(x_empty + slot);
-        tc::commit(a_empty + buf);
+        if (++xslot == T::XST) xslot = 0, xphase ^= 1;
+        if (++abuf == T::kABufs) abuf = 0, aphase ^= 1;
       }
-      tc::commit(done);
-      if (!ok)
-        for (int n = 0; n < 100000 && !mbar_try_wait(done, 0); ++n) {
+      if (leader) tc::commit(done + dbuf);
+      if (!ok)  // products in flight end before the tensor memory is freed
+        for (int c = 0; c < 100000 && !mbar_try_wait(done + dbuf, dphase ^ 1); ++c) {
         }
+      __syncwarp();
+      if (++dbuf == T::kDBufs) dbuf = 0, dphase ^= 1;
     }
   } else {
     // decode: thread = matrix row r0 + 32 (warp mod 4) + lane, warpgroup = step parity
     const int wg = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
-    const int64_t row = (int64_t)expert * p.n + min(r0 + r, p.n - 1);
-    const uint8_t* scales = p.w + row * p.pitch + p.k / 2;
     const int blocks = p.k / 32;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    // 16 scales; zero behind the row's last, where the copies bring zero codes
-    auto fetch = [&](int g) {
-      if (g * 16 >= blocks) return make_uint4(0, 0, 0, 0);
-      uint4 v = *reinterpret_cast<const uint4*>(scales + g * 16);
-      const int left = blocks - g * 16;
-      if (left < 16) {
-        auto keep = [&](int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : ~0u >> (32 - 8 * n); };
-        v.x &= keep(left);
-        v.y &= keep(left - 4);
-        v.z &= keep(left - 8);
-        v.w &= keep(left - 12);
-      }
-      return v;
-    };
     const uint8_t* my_codes = ring + r * (T::KW / 2);
     constexpr int kChunks = T::KS / 32;  // 16-byte chunks of a step
-    uint4 sc = fetch(k_begin / 512), next = make_uint4(0, 0, 0, 0);
     bool ok = true;
-    int slot = 0, phase = 0, mine = 0;  // `mine`: steps that this warpgroup has taken
+    int slot = 0, phase = 0, dbuf = 0, dphase = 0;
+    int taken = 0;  // steps of the jobs so far: the A buffers go round with them
+    for (int n = first_job; n < jobs && ok; n = T::kStay ? n + job_step : jobs) {
+      job = n == first_job ? first : find_job(n);
+      const int64_t row = (int64_t)job.expert * p.n + min(job.r0 + r, p.n - 1);
+      const uint8_t* scales = p.w + row * p.pitch + p.k / 2;
+      // 16 scales; zero behind the row's last, where the copies bring zero codes
+      auto fetch = [&](int g) {
+        if (g * 16 >= blocks) return make_uint4(0, 0, 0, 0);
+        uint4 v = *reinterpret_cast<const uint4*>(scales + g * 16);
+        const int left = blocks - g * 16;
+        if (left < 16) {
+          auto keep = [&](int b) { return b >= 4 ? ~0u : b <= 0 ? 0u : ~0u >> (32 - 8 * b); };
+          v.x &= keep(left);
+          v.y &= keep(left - 4);
+          v.z &= keep(left - 8);
+          v.w &= keep(left - 12);
+        }
+        return v;
+      };
+      uint4 sc = fetch(k_begin / 512), next = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-    for (int first = 0; first < stages && ok; first += T::kSteps) {  // a copy of 256 weights
-      const bool odd = (first / T::kSteps) & 1;
-      if (!odd) next = fetch(k_begin / 512 + first / (2 * T::kSteps) + 1);
-      const uint32_t lo = odd ? sc.z : sc.x, hi = odd ? sc.w : sc.y;  // the copy's 8 scales
-      // the same way for the whole warp: its stores to tensor memory go together
-      const bool big = __any_sync(0xffffffffu, (over128(lo) | over128(hi)) != 0);
-      ok = tc::wait_warp(w_full + slot, phase, &gave_up);
+      for (int first = 0; first < steps && ok; first += T::kSteps) {  // a copy of 256 weights
+        const bool odd = (first / T::kSteps) & 1;
+        if (!odd) next = fetch(k_begin / 512 + first / (2 * T::kSteps) + 1);
+        const uint32_t lo = odd ? sc.z : sc.x, hi = odd ? sc.w : sc.y;  // the copy's 8 scales
+        // the same way for the whole warp: its stores to tensor memory go together
+        const bool big = __any_sync(0xffffffffu, (over128(lo) | over128(hi)) != 0);
+        ok = tc::wait_warp(w_full + slot, phase, &gave_up);
 #pragma unroll
-      for (int u = 0; u < T::kSteps / 2; ++u) {
-        const int h = 2 * u + wg;
-        if (!ok || first + h >= stages) continue;
-        uint4 q[kChunks];
+        for (int u = 0; u < T::kSteps / 2; ++u) {
+          const int h = 2 * u + wg;
+          if (!ok || first + h >= steps) continue;
+          const int step = taken + first + h;
+          uint4 q[kChunks];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)  // the 128-byte swizzle: chunk c of row r at c ^ (r mod 8)
-          q[c] = *reinterpret_cast<const uint4*>(my_codes + slot * T::kWBytes +
-                                                 ((h * kChunks + c) ^ (r & 7)) * 16);
-        const uint32_t word = kChunks == 4 ? (wg ? hi : lo) : (u ? hi : lo) >> (16 * wg);
-        const int buf = (2 * mine + wg) % T::kABufs;
-        const uint32_t free = (2 * mine / T::kABufs & 1) ^ 1, at = lane_addr + buf * T::kACols;
-        ok = big ? decode_step<kChunks, true>(q, word, p.four, at, a_empty + buf, free, &gave_up)
-                 : decode_step<kChunks, false>(q, word, p.four, at, a_empty + buf, free, &gave_up);
-        if (!ok) continue;
-        ++mine;
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(a_full + buf);
+          for (int c = 0; c < kChunks; ++c)  // 128-byte swizzle: chunk c of row r at c ^ (r mod 8)
+            q[c] = *reinterpret_cast<const uint4*>(my_codes + slot * T::kWBytes +
+                                                   ((h * kChunks + c) ^ (r & 7)) * 16);
+          const uint32_t word = kChunks == 4 ? (wg ? hi : lo) : (u ? hi : lo) >> (16 * wg);
+          const int buf = step % T::kABufs;
+          const uint32_t free = (step / T::kABufs & 1) ^ 1, at = lane_addr + buf * T::kACols;
+          ok = big ? decode_step<kChunks, true>(q, word, p.four, at, a_empty + buf, free, &gave_up)
+                   : decode_step<kChunks, false>(q, word, p.four, at, a_empty + buf, free, &gave_up);
+          if (!ok) continue;
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(a_full + buf);
+        }
+        if (lane == 0) mbar_arrive(w_empty + slot);
+        if (++slot == T::WST) slot = 0, phase ^= 1;
+        if (odd) sc = next;
       }
-      if (lane == 0) mbar_arrive(w_empty + slot);
-      if (++slot == T::WST) slot = 0, phase ^= 1;
-      if (odd) sc = next;
-    }
-    __syncwarp();
-    // the sums: warpgroup = half of the rows of x
-    ok = ok && (stages == 0 || tc::wait_warp(done, 0, &gave_up));
-    tc::fence_after();
-    Out* out = static_cast<Out*>(p.out);
-    float* part = reinterpret_cast<float*>(ring);  // split along k: [N][128], ring is idle
-    constexpr int kStep = N >= 64 ? 32 : 8;
-    for (int c0 = wg * (N / 2); c0 < min((wg + 1) * (N / 2), nt); c0 += kStep) {
-      uint32_t v[kStep];
+      taken += steps;
       __syncwarp();
-      if (kStep == 32) tc::tmem_ld32(lane_addr + T::kDCol + c0, v);
-      else tc::tmem_ld8(lane_addr + T::kDCol + c0, v);
-      tc::wait_ld();
+      // the sums: warpgroup = half of the rows of x
+      ok = ok && tc::wait_warp(done + dbuf, dphase, &gave_up);
+      if (!ok) break;
+      tc::fence_after();
+      Out* out = static_cast<Out*>(p.out);
+      float* part = reinterpret_cast<float*>(ring);  // split along k: [N][128], ring is idle
+      constexpr int kStep = N >= 64 ? 32 : 8;
+      const uint32_t d_addr = lane_addr + T::kDCol + dbuf * N;
+      for (int c0 = wg * (N / 2); c0 < min((wg + 1) * (N / 2), job.nt); c0 += kStep) {
+        uint32_t v[kStep];
+        __syncwarp();
+        if (kStep == 32) tc::tmem_ld32(d_addr + c0, v);
+        else tc::tmem_ld8(d_addr + c0, v);
+        tc::wait_ld();
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        const float f = stages == 0 ? 0.f : __uint_as_float(v[j]);
-        if (p.splits > 1) {
-          part[(c0 + j) * kRows + r] = f;
-        } else if (ok && c0 + j < nt && r0 + r < p.n) {
-          put(out + (int64_t)(t0 + c0 + j) * p.out_stride + r0 + r, f);
+        for (int j = 0; j < kStep; ++j) {
+          const float f = __uint_as_float(v[j]);
+          if (p.splits > 1) {
+            part[(c0 + j) * kRows + r] = f;
+          } else if (c0 + j < job.nt && job.r0 + r < p.n) {
+            put(out + (int64_t)(job.t0 + c0 + j) * p.out_stride + job.r0 + r, f);
+          }
         }
       }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(d_free + dbuf);
+      if (++dbuf == T::kDBufs) dbuf = 0, dphase ^= 1;
     }
   }
   tc::fence_before();
@@ -436,12 +491,12 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
     // every CTA joins its share of the rows of x, always adding the parts in the same order
     cluster_sync();
     const int r = threadIdx.x & (kRows - 1);
-    if (threadIdx.x < 2 * kRows && r0 + r < p.n) {
-      for (int j = split * 2 + (threadIdx.x >> 7); j < nt; j += 2 * p.splits) {
+    if (threadIdx.x < 2 * kRows && job.r0 + r < p.n) {
+      for (int j = split * 2 + (threadIdx.x >> 7); j < job.nt; j += 2 * p.splits) {
         float sum = 0.f;
         for (int s = 0; s < p.splits; ++s)
           sum += ld_cluster(smem_u32(ring) + (uint32_t)(j * kRows + r) * 4, s);
-        put(static_cast<Out*>(p.out) + (int64_t)(t0 + j) * p.out_stride + r0 + r, sum);
+        put(static_cast<Out*>(p.out) + (int64_t)(job.t0 + j) * p.out_stride + job.r0 + r, sum);
       }
     }
     cluster_sync();
@@ -451,7 +506,7 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
 
 template <int N, class Out>
 tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap,
-                  const CUtensorMap& wmap, cudaStream_t stream) {
+                  const CUtensorMap& wmap, int sms, cudaStream_t stream) {
   using T = Tile<N>;
   auto kernel = mxfp4_matmul_kernel<N, Out>;
   static std::atomic<uint64_t> devices;
@@ -460,8 +515,9 @@ tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap
   cudaLaunchConfig_t c = {};
   const int64_t tiles = p.offsets ? (int64_t)p.rows / N + std::min<int64_t>(p.n_experts, p.rows)
                                   : ((int64_t)p.rows + N - 1) / N;
-  OP_ARG(tiles <= 65535, op, "too many rows for one call");
-  c.gridDim = dim3((unsigned)((p.n + kRows - 1) / kRows * p.splits), (unsigned)tiles);
+  const int64_t jobs = tiles * ((p.n + kRows - 1) / kRows);
+  OP_ARG(jobs < ((int64_t)1 << 30), op, "too many rows for one call");
+  c.gridDim = dim3((unsigned)(T::kStay ? std::min<int64_t>(jobs, sms) : jobs * p.splits));
   c.blockDim = dim3(kThreadsMm);
   c.dynamicSmemBytes = T::kSmem;
   c.stream = stream;
@@ -541,8 +597,8 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
 #define MM(N)                                                                            \
   case N:                                                                                \
     return out_type == TRE_BF16                                                          \
-               ? launch<N, __nv_bfloat16>(op, p, xmap, wmap, (cudaStream_t)stream)       \
-               : launch<N, float>(op, p, xmap, wmap, (cudaStream_t)stream)
+               ? launch<N, __nv_bfloat16>(op, p, xmap, wmap, sms, (cudaStream_t)stream)       \
+               : launch<N, float>(op, p, xmap, wmap, sms, (cudaStream_t)stream)
   switch (tile) {
     MM(16);
     MM(32);

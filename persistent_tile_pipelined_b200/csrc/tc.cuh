@@ -194,6 +194,18 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The same from its two halves: the upper is a constant of the layout, the lower moves by
+// bytes / 16.
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo) {
+  return (sbo >> 4) | (1u << 14) | (2u << 29);
+}
+__device__ __forceinline__ constexpr uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  return (uint64_t)hi << 32 | lo;
+}
+
 // D (tensor memory) = or += A (shared) B (shared), by one thread.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool add) {
