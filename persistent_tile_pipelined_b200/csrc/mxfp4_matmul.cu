@@ -20,7 +20,7 @@ namespace tre {
 namespace {
 
 constexpr int kRows = 128;          // matrix rows per CTA
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kThreadsMm = 320;  // warps 0-7: two decode warpgroups
+constexpr int kDecodeWarps = 8;     // warps 0-7: two warpgroups
 
 template <int N>
 struct Tile {
@@ -36,7 +36,13 @@ struct Tile {
   static constexpr int kDCol = kABufs * kACols;
   static constexpr int kXBytes = N * KS * 2, kWBytes = kRows * KW / 2;
   static constexpr int kSmem = WST * kWBytes + XST * kXBytes + 1024 + 512;
-  static constexpr bool kStay = N == 256;            // a CTA takes job after job
+  // The largest tile has the SM to itself: a CTA stays and takes job after job, and two
+  // warpgroups of their own carry the sums out while the next job's products run (its sums
+  // take half of the tensor memory, so they have to be out of it first).
+  static constexpr bool kStay = N == 256;
+  static constexpr int kOutWarps = kStay ? 8 : 0;
+  static constexpr int kCopyWarp = kDecodeWarps + kOutWarps, kMmaWarp = kCopyWarp + 1;
+  static constexpr int kThreads = kStay ? 640 : 320; // (whole warpgroups where registers move)
   static constexpr int kCtas = N == 256 ? 1 : 2;     // per SM
   static_assert(kDCol + kDBufs * N <= kCols, "tensor memory");
   static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory");
@@ -159,7 +165,7 @@ struct Job {
 };
 
 template <int N, class Out>
-__global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
+__global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap xmap,
                         const __grid_constant__ CUtensorMap wmap, const MatmulParams p) {
   using T = Tile<N>;
@@ -267,10 +273,10 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
       mbar_init(d_free + i, 8);
     }
     fence_mbar_init();
-  } else if (warp == kCopyWarp && lane == 0) {
+  } else if (warp == T::kCopyWarp && lane == 0) {
     tc::prefetch_map(&wmap);
     tc::prefetch_map(&xmap);
-  } else if (warp == kMmaWarp) {
+  } else if (warp == T::kMmaWarp) {
     tc::tmem_alloc(&tmem_base, T::kCols);
   }
   tc::fence_before();
@@ -288,7 +294,10 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
 
   const int jobs = lane_last[31] * row_tiles;
   Job job{0, 0, 0, 0};  // of the reduction at the end
-  if (warp == kCopyWarp) {
+  // registers where the sums have warps of their own: 640 x 96 at launch, 256 x 80 + 256 x 136 +
+  // 128 x 40 now
+  if (T::kStay && warp >= T::kCopyWarp) tc::regs_less<40>();
+  if (warp == T::kCopyWarp) {
     // (the whole warp, one lane issues: see the products)
     const bool leader = tc::elect_one();
     int wslot = 0, wphase = 1, xslot = 0, xphase = 1;  // places and the parity that frees them
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
         for (int c = 0; c < 100000 && !mbar_try_wait(w_full + i % T::WST, i / T::WST & 1); ++c) {
         }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == T::kMmaWarp) {
     // The whole warp runs the loop, so that what the products take is uniform; one lane issues.
     const bool leader = tc::elect_one();
     constexpr uint32_t kHi = tc::desc_hi(1024);
@@ -385,7 +394,52 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
       __syncwarp();
       if (++dbuf == T::kDBufs) dbuf = 0, dphase ^= 1;
     }
+  } else if (T::kStay && warp >= kDecodeWarps) {
+    // The sums of a job: thread = matrix row, warpgroup = 128 of the rows of x.  Three
+    // quarters wait in registers so that the tensor memory is free after one is stored.
+    if (warp >= T::kMmaWarp) {
+      // (fills the last warpgroup)
+    } else {
+      if (T::kStay) tc::regs_more<136>();
+      const int wg = (warp - kDecodeWarps) >> 2, quad = warp & 3, r = quad * 32 + lane;
+      const uint32_t d_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::kDCol + wg * 128;
+      bool ok = true;
+      int phase = 0;
+      for (int n = first_job; n < jobs && ok; n += job_step) {
+        const Job j = n == first_job ? first : find_job(n);
+        ok = tc::wait_warp(done, phase, &gave_up);
+        phase ^= 1;
+        if (!ok) break;
+        tc::fence_after();
+        const int64_t stride = p.out_stride;
+        Out* out = static_cast<Out*>(p.out) + (int64_t)(j.t0 + wg * 128) * stride + j.r0 + r;
+        const int count = j.r0 + r < p.n ? j.nt - wg * 128 : 0;
+        uint32_t v[3][32];
+        auto store = [&](const uint32_t* s, int c0) {
+          Out* o = out + (int64_t)c0 * stride;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < count) put(o + c * stride, __uint_as_float(s[c]));
+        };
+        tc::tmem_ld32(d_addr, v[0]);
+        tc::tmem_ld32(d_addr + 32, v[1]);
+        tc::tmem_ld32(d_addr + 64, v[2]);
+        tc::wait_ld();
+        store(v[0], 0);
+        __syncwarp();
+        tc::tmem_ld32(d_addr + 96, v[0]);
+        tc::wait_ld();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_free);
+        store(v[1], 32);
+        store(v[2], 64);
+        store(v[0], 96);
+        __syncwarp();
+      }
+    }
   } else {
+    if (T::kStay) tc::regs_less<80>();
     // decode: thread = matrix row r0 + 32 (warp mod 4) + lane, warpgroup = step parity
     const int wg = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
@@ -450,6 +504,7 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
       }
       taken += steps;
       __syncwarp();
+      if (T::kStay) continue;
       // the sums: warpgroup = half of the rows of x
       ok = ok && tc::wait_warp(done + dbuf, dphase, &gave_up);
       if (!ok) break;
@@ -482,7 +537,7 @@ __global__ void __launch_bounds__(kThreadsMm, Tile<N>::kCtas)
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == T::kMmaWarp) {
     __syncwarp();
     tc::fence_after();
     tc::tmem_free(tmem, T::kCols);
@@ -518,7 +573,7 @@ tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap
   const int64_t jobs = tiles * ((p.n + kRows - 1) / kRows);
   OP_ARG(jobs < ((int64_t)1 << 30), op, "too many rows for one call");
   c.gridDim = dim3((unsigned)(T::kStay ? std::min<int64_t>(jobs, sms) : jobs * p.splits));
-  c.blockDim = dim3(kThreadsMm);
+  c.blockDim = dim3(T::kThreads);
   c.dynamicSmemBytes = T::kSmem;
   c.stream = stream;
   cudaLaunchAttribute attr = {};
