@@ -339,15 +339,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   } else if (warp == kCopyWarp && lane == 0 && p.a.n_kv_rows > 0) {
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
+  } else if (warp == kMmaWarp) {
+    tc::tmem_alloc(&tmem_base, 512);
   }
-  __syncthreads();
-  const Item it = item;
-  if (it.rows == 0) return;
-  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_base;
+  const Item it = item;
+  if (it.rows == 0) {
+    if (warp == kMmaWarp) tc::tmem_free(tmem, 512);
+    return;
+  }
 
   // keys that a row sees: it.nk - it.nq + (row / g) + 1, not below 0
   auto sees = [&](int row) { return max(it.nk - it.nq + row / g + 1, 0); };
@@ -408,7 +411,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     // Key tiles that some row sees only in part: values of keys behind the sequence become
     // zero (P is zero there, and 0 x NaN is not), others are looked through for NaN and
     // infinities.
-    int bad = 0, checked = 0;
+    uint32_t bad = 0;
+    int checked = 0;
     for (int i = max(kb, least / kTile); i < ke; ++i) {
       // the product's thread says when the tile is there (a wait on the tile's own barrier
       // could mistake an earlier round of the ring for this one)
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       const int t64 = threadIdx.x - kFixWarp * 32, ch = t64 % kLanes;
       const int from = max(least - i * kTile, 0) / kRowsAtOnce * kRowsAtOnce;
       v += (ch >> 3) * kTile * 128 + (ch & 7) * 16;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = from + t64 / kLanes; j < kTile; j += kRowsAtOnce) {
         uint4* at = reinterpret_cast<uint4*>(v + j * 128);
         if (i * kTile + j >= it.nk) {
@@ -427,15 +431,15 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
           const uint4 x = *at;
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+          for (int e = 0; e < 4; ++e)  // an exponent of ones carries into the sign's place
+            bad |= (w[e] & 0x7f807f80u) + 0x00800080u;
         }
       }
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_fixed);
     }
-    if (bad) poison = 1;
+    if (bad & 0x80008000u) poison = 1;
   } else {
     tc::regs_more<208>();
     const int sub = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
@@ -446,28 +450,27 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     const int n_mine = sub == 0 ? n_sub[0] : n_sub[1];
     if (sub < subs && kb < n_mine) {
       // this tile's rows of q, 16 bytes a lane, swizzled; rows that do not exist are zero
-      constexpr int kChunks = D / 8, kPass = kTile / kChunks, kBatch = 8;
+      constexpr int kChunks = D / 8, kPass = kTile / kChunks;
       const int ch = r % kChunks, r8 = r / kChunks;
+      const int at = it.row0 + sub * kTile + r8, dt = kPass / g, dh = kPass - dt * g;
+      int tk = at / g, hd = at - tk * g;
+      const __nv_bfloat16* src = p.q + (int64_t)kh * g * p.a.q_head_stride + ch * 8;
+      uint4 val[kChunks];  // all loads in flight together
+#pragma unroll
+      for (int x = 0; x < kChunks; ++x) {
+        val[x] = make_uint4(0, 0, 0, 0);
+        if (sub * kTile + r8 + x * kPass < it.rows)
+          val[x] = *reinterpret_cast<const uint4*>(src + (int64_t)(it.q0 + tk) * p.a.q_row_stride +
+                                                   (int64_t)hd * p.a.q_head_stride);
+        tk += dt;
+        hd += dh;
+        if (hd >= g) hd -= g, ++tk;
+      }
       uint8_t* dst = qs + sub * T::kTileBytes + (ch >> 3) * kTile * 128;
 #pragma unroll
-      for (int x = 0; x < kChunks; x += kBatch) {
-        uint4 val[kBatch];  // loads in flight together
-#pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-          const int gr = sub * kTile + r8 + (x + y) * kPass;
-          val[y] = make_uint4(0, 0, 0, 0);
-          if (gr < it.rows) {
-            const uint32_t at = (uint32_t)(it.row0 + gr), tk = at / (uint32_t)g;
-            val[y] = *reinterpret_cast<const uint4*>(
-                p.q + (int64_t)(it.q0 + (int)tk) * p.a.q_row_stride +
-                (int64_t)(kh * g + (int)(at - tk * g)) * p.a.q_head_stride + ch * 8);
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-          const int rr = r8 + (x + y) * kPass;
-          *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) * 16)) = val[y];
-        }
+      for (int x = 0; x < kChunks; ++x) {
+        const int rr = r8 + x * kPass;
+        *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) * 16)) = val[x];
       }
       tc::fence_async_smem();
       __syncwarp();
@@ -593,6 +596,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
         }
       } else {
         const RowOut dst = row_out(p, D, split, tok, h);
+        // (a lone row tile's q place holds the other half's sums)
+        uint8_t* stage = alternate ? qs + 3 * T::kTileBytes : qs + sub * T::kTileBytes;
         float f0 = 1.f, f1 = 0.f;  // this tile's share and the other's
         if (alternate) {
           const float2 ml = other_ml[r];
@@ -622,8 +627,10 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
           if (round == 0 || see == 0)
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = 0;
-          if (mine && p.splits == 1) {
-            uint4* out = reinterpret_cast<uint4*>(dst.out + x);
+          if (p.splits == 1) {
+            // through shared memory (this row tile's q is done with, or the other's), 16 bytes
+            // a chunk, so that rows leave whole
+            uint4* row_out = reinterpret_cast<uint4*>(stage + r * D * 2);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint32_t w[4];
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
               for (int z = 0; z < 4; ++z)
                 w[z] = pack_bf16(__uint_as_float(o[8 * y + 2 * z]) * inv,
                                  __uint_as_float(o[8 * y + 2 * z + 1]) * inv);
-              out[y] = make_uint4(w[0], w[1], w[2], w[3]);
+              row_out[(x / 8 + y) ^ (r & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (mine) {
             uint4* out = reinterpret_cast<uint4*>(dst.o + x);
@@ -639,6 +646,19 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
             for (int y = 0; y < 8; ++y)
               out[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
             if (x == 0) *dst.ml = make_float2(m, see > kb * kTile && kb < ke ? l : -1.f);
+          }
+        }
+        if (p.splits == 1) {
+          __syncwarp();
+          constexpr int kChunks = D / 8, kRows2 = 32 / kChunks;  // rows of a store
+          const int ch = lane % kChunks;
+#pragma unroll 4
+          for (int x = 0; x < 32; x += kRows2) {
+            const int rr = x + lane / kChunks;  // of the warp's
+            const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst.out), rr);
+            const uint4 val = reinterpret_cast<const uint4*>(
+                stage + (quad * 32 + rr) * D * 2)[ch ^ (rr & 7)];
+            if (base + quad * 32 + rr < it.rows) reinterpret_cast<uint4*>(to)[ch] = val;
           }
         }
       }
