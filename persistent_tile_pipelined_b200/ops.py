@@ -119,7 +119,7 @@ def prompt_attention(q, k, v, q_offsets=None, kv_offsets=None, scale: Optional[f
         _need(q_offsets.numel() == kv_offsets.numel(), "q_offsets and kv_offsets differ in length")
         n = q_offsets.numel() - 1
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _tensor(out, "out", 3, (torch.bfloat16,), q.device)
         _need(out.shape == q.shape, f"out has shape {tuple(out.shape)}")
@@ -207,7 +207,7 @@ def mxfp4_matmul(x, w, offsets=None, out_dtype=torch.float32, out=None):
         _offsets(offsets, "offsets", x.device)
         _need(offsets.numel() == E + 1, f"offsets must have {E + 1} entries")
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        out = x.new_empty((T, N), dtype=out_dtype)
     else:
         _tensor(out, "out", 2, (out_dtype,), x.device)
         _need(tuple(out.shape) == (T, N), f"out has shape {tuple(out.shape)}")
@@ -231,14 +231,14 @@ def add_rmsnorm(x, delta, gain, eps: float, x_out=None, out=None):
     _need(gain.shape[0] == d, f"gain has {gain.shape[0]} entries, not {d}")
     own_x, own = x_out is None, out is None
     if own_x:
-        x_out = torch.empty((T, d), dtype=torch.float32, device=x.device)
+        x_out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif x_out is not x:
         _tensor(x_out, "x_out", 2, (torch.float32,), x.device)
         _need(x_out.shape == x.shape, f"x_out has shape {tuple(x_out.shape)}")
         if x_out.data_ptr() != x.data_ptr() or x_out.stride() != x.stride():
             _apart(x_out, "x_out", x=x)
     if own:
-        out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     else:
         _tensor(out, "out", 2, (torch.bfloat16,), x.device)
         _need(out.shape == x.shape, f"out has shape {tuple(out.shape)}")

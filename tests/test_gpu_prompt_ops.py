@@ -328,6 +328,19 @@ def test_quantize_is_exact(R, K, dtype):
         assert (back == decoded(rows, K)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_quantize_a_long_matrix_like_its_parts(dtype):
+    """Over a million groups take another form of the kernels than the parts do."""
+    w = weights(4099, 8256, dtype, 5)
+    rows = ops.mxfp4_quantize(w)
+    parts = [ops.mxfp4_quantize(p) for p in w.split(1000)]
+    assert torch.equal(rows, torch.cat(parts))
+    for out_dtype in (torch.bfloat16, torch.float32):
+        back = ops.mxfp4_dequantize(rows, 8256, out_dtype)
+        assert torch.equal(back, torch.cat([ops.mxfp4_dequantize(p, 8256, out_dtype)
+                                            for p in parts]))
+
+
 def test_quantize_strides_batches_and_bad_values():
     w = weights(24, 64, torch.float32, 1)
     wide = torch.zeros(24, 80, device=DEV)
@@ -404,6 +417,47 @@ def test_matmul(T, E, R, K, lens, dtype):
     assert y.shape == (T, R) and y.dtype == dtype
     check_matmul(y, x, w, lens, K)
     assert torch.equal(y, ops.mxfp4_matmul(x, w, off, dtype))
+
+
+# tiles of 256 rows, more of them than SMs: a CTA takes several, whose steps and copies of
+# weights end at odd places
+MANY = [(600, 1, 9000, 64, None), (1030, 4, 5100, 96, [257, 0, 513, 260]),
+        (2000, 3, 6500, 352, [1, 1500, 499]), (700, 2, 9600, 1312, [700, 0])]
+
+
+@pytest.mark.parametrize("T,E,R,K,lens", MANY, ids=lambda x: str(x) if isinstance(x, int) else "")
+def test_matmul_several_tiles_a_cta(T, E, R, K, lens):
+    x, w, off = matmul_case(T, E, R, K, lens)
+    y = ops.mxfp4_matmul(x, w, off, torch.bfloat16)
+    check_matmul(y, x, w, lens, K)
+    assert torch.equal(y, ops.mxfp4_matmul(x, w, off, torch.bfloat16))
+
+
+def test_matmul_on_two_streams_at_once():
+    cases = [matmul_case(16, 1, 512, 2048, None, seed=i) for i in range(2)]
+    cases += [matmul_case(600, 1, 9000, 64, None, seed=i) for i in range(2)]
+    want = [ops.mxfp4_matmul(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(ops.mxfp4_matmul(*c))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_matmul_large_and_small_scales_in_one_row():
+    """Scales on both sides of 1 (byte 127) and beyond 2 (128), mixed within rows and between
+    the rows of a warp."""
+    T, R, K = 20, 140, 512
+    x, w, _ = matmul_case(T, 1, R, K, None)
+    g = gen(2)
+    w[0, :, K // 2:K // 2 + K // 32] = torch.randint(100, 150, (R, K // 32), generator=g, device=DEV,
+                                                     dtype=torch.int32).to(torch.uint8)
+    w[0, 7::32, K // 2:] = 120  # rows without a large one
+    check_matmul(ops.mxfp4_matmul(x, w), x, w, None, K)
 
 
 def test_matmul_rows_of_no_expert_strides_and_bad_neighbours():
