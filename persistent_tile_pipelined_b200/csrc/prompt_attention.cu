@@ -36,8 +36,21 @@ struct Shape {
   static constexpr int kO = 2 * kTile;          // tensor-memory column of the first O
 };
 
+// Division by a number that the host knows, of numbers below 2^31: inv is ceil(2^32 / d) (0 for
+// 1), whose quotient is at most one too large.
+struct Divisor {
+  uint32_t d, inv;
+};
+
+__device__ __forceinline__ int quotient(int n, Divisor d) {
+  uint32_t q = d.inv ? __umulhi((uint32_t)n, d.inv) : (uint32_t)n;
+  if (q * d.d > (uint32_t)n) --q;
+  return (int)q;
+}
+
 struct AttnParams {
   tre_attention a;
+  Divisor group, kv_heads;  // query heads of a kv head; kv heads
   const __nv_bfloat16* q;
   const __nv_bfloat16 *k, *v;  // the slow path's view of what the tensor maps describe
   __nv_bfloat16* out;
@@ -156,7 +169,7 @@ template <int D>
 __device__ __forceinline__ void slow_row(const AttnParams& p, int split, int tok, int h, int k0,
                                          int from, int to, int see) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, kh = h / (p.a.n_q_heads / p.a.n_kv_heads);
+  const int lane = threadIdx.x & 31, kh = quotient(h, p.group);
   const __nv_bfloat16* qr =
       p.q + (int64_t)tok * p.a.q_row_stride + (int64_t)h * p.a.q_head_stride + lane;
   const __nv_bfloat16* k = p.k + (int64_t)kh * p.a.k_head_stride + lane;
@@ -309,12 +322,13 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   __shared__ int gave_up, poison;
   __shared__ Item item;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = p.a.n_q_heads / p.a.n_kv_heads;
-  const int kh = blockIdx.x % p.a.n_kv_heads;
+  const int g = (int)p.group.d;
+  const int place = quotient(blockIdx.x, p.kv_heads);  // of the row tile, from the last
+  const int kh = (int)blockIdx.x - place * p.a.n_kv_heads;
 
   if (warp == 0) {
     // the last row tiles first: with causal rows they take longest
-    const Item it = find_item(p, g, p.tiles - 1 - (int)(blockIdx.x / p.a.n_kv_heads));
+    const Item it = find_item(p, g, p.tiles - 1 - place);
     if (lane == 0) {
       item = it;
       gave_up = 0;
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   }
 
   // keys that a row sees: it.nk - it.nq + (row / g) + 1, not below 0
-  auto sees = [&](int row) { return max(it.nk - it.nq + row / g + 1, 0); };
+  auto sees = [&](int row) { return max(it.nk - it.nq + quotient(row, p.group) + 1, 0); };
   const int subs = it.rows > kTile ? 2 : 1;
   const int least = sees(it.row0);  // of the CTA's rows
   int n_sub[2];                     // key tiles of each row tile
@@ -361,8 +375,10 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   n_sub[1] = subs == 2 ? (sees(it.row0 + it.rows - 1) + kTile - 1) / kTile : 0;
   const int n_all = max(n_sub[0], n_sub[1]);
   const int split = blockIdx.y;
-  const int kb = (int)((int64_t)n_all * split / p.splits);
-  const int ke = (int)((int64_t)n_all * (split + 1) / p.splits);
+  // (below 2^24 tiles and 2^8 parts: the products fit 32 bits)
+  const int kb = p.splits == 1 ? 0 : (int)((uint32_t)n_all * (uint32_t)split / (uint32_t)p.splits);
+  const int ke = p.splits == 1 ? n_all
+                               : (int)((uint32_t)n_all * (split + 1u) / (uint32_t)p.splits);
   // One row tile alone would wait for its own softmax at every step: both take it, with the
   // even and the odd key tiles, and join their sums at the end.
   const bool alternate = subs == 1;
@@ -452,8 +468,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       // this tile's rows of q, 16 bytes a lane, swizzled; rows that do not exist are zero
       constexpr int kChunks = D / 8, kPass = kTile / kChunks;
       const int ch = r % kChunks, r8 = r / kChunks;
-      const int at = it.row0 + sub * kTile + r8, dt = kPass / g, dh = kPass - dt * g;
-      int tk = at / g, hd = at - tk * g;
+      const int at = it.row0 + sub * kTile + r8, dt = quotient(kPass, p.group), dh = kPass - dt * g;
+      int tk = quotient(at, p.group), hd = at - tk * g;
       const __nv_bfloat16* src = p.q + (int64_t)kh * g * p.a.q_head_stride + ch * 8;
       uint4 val[kChunks];  // all loads in flight together
 #pragma unroll
@@ -584,14 +600,15 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       asm volatile("bar.sync 3, 256;" ::: "memory");
     }
     const bool slow = poison != 0;
-    const int tok = it.q0 + row / g, h = kh * g + row % g;
+    const int tok0 = quotient(row, p.group), tok = it.q0 + tok0, h = kh * g + row - tok0 * g;
     if (sub < subs && ok && any_row) {
       if (slow) {
 #pragma unroll 1
         for (int x = 0; x < 32; ++x) {
           const int rx = row - lane + x, sx = sees(rx);
           if (rx - it.row0 >= it.rows) break;
-          slow_row<D>(p, split, it.q0 + rx / g, kh * g + rx % g, it.k0, min(kb * kTile, sx),
+          const int tx = quotient(rx, p.group);
+          slow_row<D>(p, split, it.q0 + tx, kh * g + rx - tx * g, it.k0, min(kb * kTile, sx),
                       min(ke * kTile, sx), sx);
         }
       } else {
@@ -678,12 +695,14 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
 // Joins the parts of the rows of one item, a warp per row, parts in order.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
-  const int g = p.a.n_q_heads / p.a.n_kv_heads, kh = blockIdx.x % p.a.n_kv_heads;
+  const int g = (int)p.group.d, place = quotient(blockIdx.x, p.kv_heads);
+  const int kh = (int)blockIdx.x - place * p.a.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Item it = find_item(p, g, (int)(blockIdx.x / p.a.n_kv_heads));
+  const Item it = find_item(p, g, place);
   const int rr = blockIdx.y * 8 + warp;
   if (rr >= it.rows) return;
-  const int row = it.row0 + rr, tok = it.q0 + row / g, h = kh * g + row % g;
+  const int row = it.row0 + rr, tok0 = quotient(row, p.group);
+  const int tok = it.q0 + tok0, h = kh * g + row - tok0 * g;
   const int64_t step = (int64_t)p.a.n_q_rows * p.a.n_q_heads;
   const int64_t at = (int64_t)tok * p.a.n_q_heads + h;
   float m = -INFINITY;
@@ -733,6 +752,11 @@ tre_status check(const char* op, const tre_attention* a) {
   return TRE_OK;
 }
 
+
+Divisor divisor(int d) {
+  return {(uint32_t)d,
+          d == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + (uint64_t)d - 1) / (uint64_t)d)};
+}
 
 // Row tiles of a kv head: an upper bound, the lengths are known on the device only.
 int row_tiles(const tre_attention& a) {
@@ -829,6 +853,8 @@ TRE_EXPORT tre_status tre_prompt_attention(const tre_attention* a, const void* q
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o +
                                         (size_t)p.splits * a->n_q_rows * a->n_q_heads * a->head_dim);
+  p.group = divisor(a->n_q_heads / a->n_kv_heads);
+  p.kv_heads = divisor(a->n_kv_heads);
   p.c = a->scale * 1.4426950408889634f;
   p.status = ops_status_ptr();
   OP_ARG(p.status, op, "the operators' status word is not available");
