@@ -471,23 +471,22 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
       const int at = it.row0 + sub * kTile + r8, dt = quotient(kPass, p.group), dh = kPass - dt * g;
       int tk = quotient(at, p.group), hd = at - tk * g;
       const __nv_bfloat16* src = p.q + (int64_t)kh * g * p.a.q_head_stride + ch * 8;
-      uint4 val[kChunks];  // all loads in flight together
+      const uint32_t dst = smem_u32(qs) + sub * T::kTileBytes + (ch >> 3) * kTile * 128;
 #pragma unroll
       for (int x = 0; x < kChunks; ++x) {
-        val[x] = make_uint4(0, 0, 0, 0);
-        if (sub * kTile + r8 + x * kPass < it.rows)
-          val[x] = *reinterpret_cast<const uint4*>(src + (int64_t)(it.q0 + tk) * p.a.q_row_stride +
-                                                   (int64_t)hd * p.a.q_head_stride);
+        // past L1, which beside this much shared memory holds less than the rows in flight
+        const int rr = r8 + x * kPass;
+        const bool there = sub * kTile + rr < it.rows;
+        tc::copy16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) * 16),
+                   src + (there ? (int64_t)(it.q0 + tk) * p.a.q_row_stride +
+                                      (int64_t)hd * p.a.q_head_stride
+                                : 0),
+                   there);
         tk += dt;
         hd += dh;
         if (hd >= g) hd -= g, ++tk;
       }
-      uint8_t* dst = qs + sub * T::kTileBytes + (ch >> 3) * kTile * 128;
-#pragma unroll
-      for (int x = 0; x < kChunks; ++x) {
-        const int rr = r8 + x * kPass;
-        *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) * 16)) = val[x];
-      }
+      tc::copy16_wait();
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full + sub);

@@ -109,6 +109,16 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* m, int x, 
       : "memory");
 }
 
+// 16 bytes from global to shared memory by this thread, or zeros; the wait is for all of its own.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Makes this thread's writes to shared memory visible to the copy and matrix units.
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
