@@ -27,14 +27,24 @@ __device__ __forceinline__ void place_of(uint32_t g, uint32_t per_row, uint32_t 
   b = g - row * per_row;
 }
 
-// 8 numbers as one 32-byte or 16-byte load.
+// 8 numbers: fp32 as one 32-byte load where the rows are aligned to that (kWide), bf16 as one of
+// 16 bytes.
+template <bool kWide>
 __device__ __forceinline__ void load8(const float* p, float* v) {
-  asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                 "=f"(v[6]), "=f"(v[7])
-               : "l"(p));
+  if (kWide) {
+    asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7])
+                 : "l"(p));
+  } else {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p + 4));
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
 }
 
+template <bool kWide>
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
   const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -47,7 +57,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
 
 // Four lanes take a group of 32 weights, 8 each: the largest magnitude by two exchanges, its
 // binary exponent from the bits, then 8 codes as one word.
-template <int kPasses, class T>
+template <int kPasses, bool kWide, class T>
 __global__ void __launch_bounds__(kRowThreads)
     mxfp4_quantize_kernel(const T* __restrict__ w, int64_t w_stride, uint32_t groups,
                           uint32_t per_row, uint32_t inv_per_row, int64_t k, int64_t pitch,
@@ -60,7 +70,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const uint32_t g = g0 + i * kGroupsPerPass;
     if (g < groups) {
       place_of(g, per_row, inv_per_row, row[i], b[i]);
-      load8(w + (int64_t)row[i] * w_stride + (int64_t)b[i] * 32 + lane4 * 8, v[i]);
+      load8<kWide>(w + (int64_t)row[i] * w_stride + (int64_t)b[i] * 32 + lane4 * 8, v[i]);
     }
   }
 #pragma unroll
@@ -160,12 +170,14 @@ void quantize(const T* w, int64_t stride, int64_t rows, int64_t k, int64_t pitch
               cudaStream_t stream) {
   const uint32_t per_row = (uint32_t)(k / 32), groups = (uint32_t)(rows * per_row);
   const uint32_t ctas = (groups + kGroupsPerPass - 1) / kGroupsPerPass;
-  if (ctas >= 4 * kLongGrid)
-    mxfp4_quantize_kernel<4><<<(ctas + 3) / 4, kRowThreads, 0, stream>>>(
-        w, stride, groups, per_row, inverse(per_row), k, pitch, out);
-  else
-    mxfp4_quantize_kernel<1><<<ctas, kRowThreads, 0, stream>>>(w, stride, groups, per_row,
-                                                               inverse(per_row), k, pitch, out);
+  const bool wide = sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(w) & 31u) == 0 &&
+                    (rows == 1 || stride % 8 == 0);
+  const uint32_t grid = ctas >= 4 * kLongGrid ? (ctas + 3) / 4 : ctas;
+  auto kernel = ctas >= 4 * kLongGrid
+                    ? (wide ? mxfp4_quantize_kernel<4, true, T> : mxfp4_quantize_kernel<4, false, T>)
+                    : (wide ? mxfp4_quantize_kernel<1, true, T> : mxfp4_quantize_kernel<1, false, T>);
+  kernel<<<grid, kRowThreads, 0, stream>>>(w, stride, groups, per_row, inverse(per_row), k, pitch,
+                                           out);
 }
 
 template <class T>

@@ -54,6 +54,7 @@ struct MatmulParams {
   void* out;
   int64_t out_stride, pitch;
   int32_t rows, n, k, n_experts, splits;
+  int32_t most_jobs;  // tiles of x times tiles of matrix rows: an upper bound
   uint32_t four;  // 4 (see e2m1x8)
   int32_t* status;
 };
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
         bounds(e + i, lane * per, lo, hi);
         tiles += (hi - lo + N - 1) / N;
       }
+      tiles = min(tiles, 1 << 25);  // (offsets that decrease cannot make the sums overflow)
     }
     int sum = tiles;
 #pragma unroll
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
     lane_last[lane] = sum;
     __syncwarp();
     Job j{0, 0, 0, 0};
-    if (first_job < lane_last[31] * row_tiles) j = find_job(first_job);
+    if (first_job < (int64_t)lane_last[31] * row_tiles) j = find_job(first_job);
     if (lane == 0) {
       gave_up = 0;
       first = j;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
   const int steps = (k_end - k_begin + T::KS - 1) / T::KS;
   const int copies = (steps + T::kSteps - 1) / T::kSteps;
 
-  const int jobs = lane_last[31] * row_tiles;
+  const int jobs = (int)min((int64_t)lane_last[31] * row_tiles, (int64_t)p.most_jobs);
   Job job{0, 0, 0, 0};  // of the reduction at the end
   // registers where the sums have warps of their own: 640 x 96 at launch, 256 x 80 + 256 x 136 +
   // 128 x 40 now
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
 }
 
 template <int N, class Out>
-tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap,
+tre_status launch(const char* op, MatmulParams p, const CUtensorMap& xmap,
                   const CUtensorMap& wmap, int sms, cudaStream_t stream) {
   using T = Tile<N>;
   auto kernel = mxfp4_matmul_kernel<N, Out>;
@@ -571,7 +573,8 @@ tre_status launch(const char* op, const MatmulParams& p, const CUtensorMap& xmap
   const int64_t tiles = p.offsets ? (int64_t)p.rows / N + std::min<int64_t>(p.n_experts, p.rows)
                                   : ((int64_t)p.rows + N - 1) / N;
   const int64_t jobs = tiles * ((p.n + kRows - 1) / kRows);
-  OP_ARG(jobs < ((int64_t)1 << 30), op, "too many rows for one call");
+  OP_ARG(jobs < ((int64_t)1 << 28), op, "too many rows for one call");
+  p.most_jobs = (int32_t)jobs;
   c.gridDim = dim3((unsigned)(T::kStay ? std::min<int64_t>(jobs, sms) : jobs * p.splits));
   c.blockDim = dim3(T::kThreads);
   c.dynamicSmemBytes = T::kSmem;
@@ -626,7 +629,7 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
   const int64_t pitch = (k / 2 + k / 32 + 15) / 16 * 16;
   const int sms = device_sms();
   MatmulParams p{static_cast<const uint8_t*>(w), offsets, out, out_row_stride, pitch,
-                 (int32_t)rows, (int32_t)n, (int32_t)k, n_experts, 1, 4u, ops_status_ptr()};
+                 (int32_t)rows, (int32_t)n, (int32_t)k, n_experts, 1, 0, 4u, ops_status_ptr()};
   OP_ARG(p.status, op, "the operators' status word is not available");
   const int tile = tile_rows(p, sms);
   if (tile <= 32) {  // few tiles: split k over a cluster until the device is busy

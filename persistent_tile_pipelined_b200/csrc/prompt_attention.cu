@@ -735,7 +735,9 @@ tre_status check(const char* op, const tre_attention* a) {
          op, "n_q_heads must be a positive multiple of n_kv_heads");
   OP_ARG(a->n_seqs >= 0 && a->n_seqs < (1 << 20), op, "n_seqs out of range");
   OP_ARG(a->n_q_rows >= 0 && a->n_kv_rows >= 0, op, "negative row count");
-  OP_ARG((int64_t)a->n_q_rows * a->n_q_heads < ((int64_t)1 << 31), op, "too many query rows");
+  OP_ARG((int64_t)a->n_q_rows * a->n_q_heads <= ((int64_t)1 << 30) &&
+             a->n_kv_rows <= (1 << 30),
+         op, "more than 2^30 rows");
   OP_ARG(a->scale > 0.f && a->scale < 3e38f, op, "scale must be positive and finite");
   const struct {
     int64_t stride;
@@ -748,6 +750,10 @@ tre_status check(const char* op, const tre_attention* a) {
     OP_ARG(d.count <= 1 || (d.stride >= a->head_dim && d.stride % 8 == 0 &&
                             d.stride < ((int64_t)1 << 38)),
            op, "rows and heads must lie apart by whole 16-byte units");
+  OP_ARG(a->n_q_rows <= 1 || a->n_q_heads <= 1 ||
+             a->out_row_stride >= (a->n_q_heads - 1) * a->out_head_stride + a->head_dim ||
+             a->out_head_stride >= (a->n_q_rows - 1) * a->out_row_stride + a->head_dim,
+         op, "output rows and heads overlap");
   return TRE_OK;
 }
 

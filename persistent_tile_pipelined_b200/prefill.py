@@ -132,8 +132,8 @@ def _out(x_out, x):
 def prefill(eng, tokens, pos: int = 0, x_out=None) -> None:
     """Fill eng's caches with the keys and values of `tokens` at positions pos .. pos + T - 1
     (the caches hold [0, pos) on entry), enqueued on torch's current stream of the engine's
-    device.  tokens: a list of ids, or a one-dimensional integer tensor (ids of a device
-    tensor are not checked against the vocabulary).  x_out (fp32 [T][hidden], optional)
+    device.  tokens: a list of ids, or a one-dimensional integer tensor (a device tensor's ids
+    are read back once, to be checked against the vocabulary).  x_out (fp32 [T][hidden], optional)
     receives the residual stream after the last layer.  GQA stacks with bf16 projections and
     MoE stacks with MXFP4 experts."""
     cfg = eng.cfg
@@ -147,8 +147,7 @@ def prefill(eng, tokens, pos: int = 0, x_out=None) -> None:
         _refuse(tre.TRE_ERR_INVALID_ARG, "tokens must be one-dimensional and whole numbers")
     T = tokens.numel()
     _check(eng, T, pos)
-    if not tokens.is_cuda and T and not (0 <= int(tokens.min()) and
-                                         int(tokens.max()) < cfg.vocab):
+    if T and not (0 <= int(tokens.min()) and int(tokens.max()) < cfg.vocab):
         _refuse(tre.TRE_ERR_INVALID_ARG, f"a token is outside [0, {cfg.vocab})")
     if T == 0:
         return

@@ -242,6 +242,71 @@ def test_attention_on_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_attention_strides_beyond_32_bits():
+    """Heads and rows that lie more than 2^31 elements apart."""
+    g = gen(12)
+    far = 2 ** 31 + 4096
+    big = torch.empty(far + 2 ** 20, dtype=torch.bfloat16, device=DEV)
+    k, v = (big.as_strided((2, 300, 64), (far, 128, 1), at) for at in (0, 64))
+    k.copy_(normal(g, 2, 300, 64))
+    v.copy_(normal(g, 2, 300, 64))
+    q = normal(g, 140, 4, 64)
+    check_attention(ops.prompt_attention(q, k, v), q, k, v, [140], [300])
+    qf = big.as_strided((2, 4, 64), (far, 64, 1), 600 * 128)  # two rows, far apart
+    qf.copy_(q[:2])
+    of = big.as_strided((2, 4, 64), (far, 64, 1), 700 * 128)
+    got = torch.empty_like(qf)
+    ops.prompt_attention(qf, k, v, out=got)
+    check_attention(got, q[:2], k, v, [2], [300])
+    with pytest.raises(ValueError):  # the spans of out and the cache overlap
+        ops.prompt_attention(qf, k, v, out=of)
+
+
+@pytest.mark.parametrize("what", ["attention", "split", "product", "cluster", "quantize", "norm"])
+def test_first_call_of_a_process_is_captured(what):
+    """No operator needs a call before the one that a graph records."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path.insert(0, sys.argv[2])
+from persistent_tile_pipelined_b200 import ops, tre
+what = sys.argv[1]
+r = lambda *s: torch.randn(s, device="cuda").bfloat16()
+if what == "attention":
+    q, k, v = r(200, 4, 64), r(2, 200, 64), r(2, 200, 64)
+    f = lambda: ops.prompt_attention(q, k, v)
+elif what == "split":
+    q, k, v = r(1, 4, 128), r(2, 9000, 128), r(2, 9000, 128)
+    f = lambda: ops.prompt_attention(q, k, v)
+elif what in ("product", "cluster"):
+    x = r(300 if what == "product" else 1, 1024)
+    w = torch.randint(100, 120, (256, 544), dtype=torch.uint8, device="cuda")
+    f = lambda: ops.mxfp4_matmul(x, w)
+elif what == "quantize":
+    w = r(64, 256)
+    f = lambda: ops.mxfp4_dequantize(ops.mxfp4_quantize(w), 256)
+else:
+    x, g = torch.randn(9, 64, device="cuda"), r(64)
+    f = lambda: ops.add_rmsnorm(x, None, g, 1e-5)[1]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = f()
+for _ in range(2):
+    graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, f())
+assert tre.tre_ops_status() == 0
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code, what, root], capture_output=True, text=True,
+                         timeout=120)
+    assert run.returncode == 0 and "same" in run.stdout, run.stderr[-2000:]
+
+
 def test_attention_refuses():
     g = gen(1)
     q, kv = normal(g, 5, 4, 64), normal(g, 2, 9, 64)
@@ -347,6 +412,13 @@ def test_quantize_strides_batches_and_bad_values():
     wide[:, :64] = w
     want = ops.mxfp4_quantize(w)
     assert torch.equal(ops.mxfp4_quantize(wide[:, :64]), want)
+    for at, pad in ((4, 20), (8, 16), (4, 24)):  # rows at 16 bytes of every 32, or some of them
+        off = torch.zeros(24, 64 + pad, device=DEV)[:, at:at + 64]
+        off.copy_(w)
+        assert torch.equal(ops.mxfp4_quantize(off), want)
+        half = torch.zeros(24, 64 + 2 * pad, device=DEV, dtype=torch.bfloat16)[:, 2 * at:2 * at + 64]
+        half.copy_(w)
+        assert torch.equal(ops.mxfp4_quantize(half), ops.mxfp4_quantize(w.bfloat16()))
     assert torch.equal(ops.mxfp4_quantize(w.view(2, 3, 4, 64)), want.view(2, 3, 4, -1))
     assert torch.equal(ops.mxfp4_quantize(w[0]), want[0])
     out = torch.full((26, mxfp4_pitch(64)), 9, dtype=torch.uint8, device=DEV)

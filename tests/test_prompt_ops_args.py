@@ -32,6 +32,7 @@ def test_attention_descriptor_is_accepted_by_the_workspace_query():
     dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
     dict(q_row_stride=1028), dict(k_row_stride=4), dict(v_head_stride=-128),
     dict(out_head_stride=127), dict(k_row_stride=0), dict(out_row_stride=64),
+    dict(out_row_stride=256, out_head_stride=128), dict(n_q_rows=1 << 28), dict(n_kv_rows=(1 << 30) + 1),
 ], ids=str)
 def test_attention_refuses(over):
     a = attention(**over)
