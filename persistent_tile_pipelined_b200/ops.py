@@ -26,11 +26,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _SMS = {}  # device index -> SM count
 
 
-def _need(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
-
-
 def _tensor(t, name: str, ndim: int, dtypes, device=None) -> None:
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -61,7 +56,8 @@ def _apart(out, name: str, /, **inputs) -> None:
     for key, t in inputs.items():
         if t is not None:
             c, d = _span(t)
-            _need(b <= c or d <= a, f"{name} may not overlap {key}")
+            if c < b and a < d:
+                raise ValueError(f"{name} may not overlap {key}")
 
 
 def _ptr(t) -> Optional[int]:
@@ -89,7 +85,8 @@ def _sms(device) -> int:
 
 def _offsets(t, name: str, device) -> None:
     _tensor(t, name, 1, (torch.int32,), device)
-    _need(t.numel() >= 2, f"{name} must have at least 2 entries")
+    if t.numel() < 2:
+        raise ValueError(f"{name} must have at least 2 entries")
 
 
 def prompt_attention(q, k, v, q_offsets=None, kv_offsets=None, scale: Optional[float] = None,
@@ -109,22 +106,25 @@ def prompt_attention(q, k, v, q_offsets=None, kv_offsets=None, scale: Optional[f
     _tensor(v, "v", 3, (torch.bfloat16,), q.device)
     T, Hq, D = q.shape
     Hkv, S, _ = k.shape
-    _need(k.shape == v.shape and k.shape[2] == D,
-          f"shapes do not fit: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    _need((q_offsets is None) == (kv_offsets is None), "q_offsets and kv_offsets go together")
+    if k.shape != v.shape or k.shape[2] != D:
+        raise ValueError(f"shapes do not fit: q {tuple(q.shape)}, k {tuple(k.shape)}, "
+                         f"v {tuple(v.shape)}")
+    if (q_offsets is None) != (kv_offsets is None):
+        raise ValueError("q_offsets and kv_offsets go together")
     n = 0
     if q_offsets is not None:
         _offsets(q_offsets, "q_offsets", q.device)
         _offsets(kv_offsets, "kv_offsets", q.device)
-        _need(q_offsets.numel() == kv_offsets.numel(), "q_offsets and kv_offsets differ in length")
+        if q_offsets.numel() != kv_offsets.numel():
+            raise ValueError("q_offsets and kv_offsets differ in length")
         n = q_offsets.numel() - 1
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _tensor(out, "out", 3, (torch.bfloat16,), q.device)
-        _need(out.shape == q.shape, f"out has shape {tuple(out.shape)}")
-        _need(T <= 1 or out.stride(0) >= D and (Hq <= 1 or out.stride(1) >= D), "out overlaps itself")
-        _apart(out, "out", q=q, k=k, v=v)
+        if out.shape != q.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}")
+        _apart(out, "out", q=q, k=k, v=v, q_offsets=q_offsets, kv_offsets=kv_offsets)
     a = tre.tre_attention(Hq, Hkv, D, n, T, S, q.stride(0), q.stride(1), k.stride(1), k.stride(0),
                           v.stride(1), v.stride(0), out.stride(0), out.stride(1),
                           1.0 / math.sqrt(D) if scale is None else scale)
@@ -140,18 +140,20 @@ def mxfp4_quantize(w, out=None):
     [..., mxfp4_pitch(K)]: per 32 weights the scale 2^(floor(log2(max)) - 2), codes to the
     nearest (ties to even), larger magnitudes saturated; a group with a NaN or an infinity
     stands for NaN."""
-    _need(isinstance(w, torch.Tensor) and w.ndim >= 1, "w must be a tensor of at least one row")
+    if not isinstance(w, torch.Tensor) or w.ndim < 1:
+        raise ValueError("w must be a tensor of at least one row")
     flat = w.reshape(-1, w.shape[-1]) if w.numel() else w.new_empty((0, w.shape[-1]))
     _tensor(flat, "w", 2, tuple(_TYPES))
     R, K = flat.shape
-    _need(K > 0 and K % 32 == 0, f"rows must have a positive multiple of 32 weights, not {K}")
+    if K <= 0 or K % 32:
+        raise ValueError(f"rows must have a positive multiple of 32 weights, not {K}")
     shape = (*w.shape[:-1], mxfp4_pitch(K))
     if out is None:
         out = torch.empty(shape, dtype=torch.uint8, device=w.device)
     else:
         _tensor(out, "out", len(shape), (torch.uint8,), w.device)
-        _need(tuple(out.shape) == shape and out.is_contiguous(),
-              f"out must be contiguous and of shape {shape}")
+        if tuple(out.shape) != shape or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous and of shape {shape}")
         _apart(out, "out", w=flat)
     _call(tre.lib.tre_mxfp4_quantize, w.device, flat.data_ptr(), _TYPES[w.dtype], R, K,
           flat.stride(0), out.data_ptr())
@@ -161,24 +163,28 @@ def mxfp4_quantize(w, out=None):
 def _rows(w, name: str, ndim: Optional[int], K: int) -> None:
     _tensor(w, name, w.ndim if ndim is None and isinstance(w, torch.Tensor) else ndim or 1,
             (torch.uint8,))
-    _need(K > 0 and K % 32 == 0, f"k must be a positive multiple of 32, not {K}")
-    _need(w.shape[-1] == mxfp4_pitch(K),
-          f"{name}'s rows of {K} weights have {mxfp4_pitch(K)} bytes, not {w.shape[-1]}")
-    _need(w.is_contiguous(), f"{name} must be contiguous")
+    if K <= 0 or K % 32:
+        raise ValueError(f"k must be a positive multiple of 32, not {K}")
+    if w.shape[-1] != mxfp4_pitch(K):
+        raise ValueError(f"{name}'s rows of {K} weights have {mxfp4_pitch(K)} bytes, "
+                         f"not {w.shape[-1]}")
+    if not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def mxfp4_dequantize(w, k: int, out_dtype=torch.bfloat16, out=None):
     """The numbers that MXFP4 rows [..., mxfp4_pitch(k)] stand for, [..., k] in bf16 or fp32
     (exact in both)."""
     _rows(w, "w", None, k)
-    _need(out_dtype in _TYPES, f"out_dtype {out_dtype} is not bf16 or fp32")
+    if out_dtype not in _TYPES:
+        raise ValueError(f"out_dtype {out_dtype} is not bf16 or fp32")
     shape = (*w.shape[:-1], k)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=w.device)
     else:
         _tensor(out, "out", len(shape), (out_dtype,), w.device)
-        _need(tuple(out.shape) == shape and out.is_contiguous(),
-              f"out must be contiguous and of shape {shape}")
+        if tuple(out.shape) != shape or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous and of shape {shape}")
         _apart(out, "out", w=w)
     _call(tre.lib.tre_mxfp4_dequantize, w.device, w.data_ptr(), w.numel() // w.shape[-1], k,
           _TYPES[out_dtype], out.data_ptr())
@@ -198,19 +204,25 @@ def mxfp4_matmul(x, w, offsets=None, out_dtype=torch.float32, out=None):
     if isinstance(w, torch.Tensor) and w.ndim == 2:
         w = w.unsqueeze(0)
     _rows(w, "w", 3, K)
-    _need(w.device == x.device, f"w is on {w.device}, not on {x.device}")
+    if w.device != x.device:
+        raise ValueError(f"w is on {w.device}, not on {x.device}")
     E, N, _ = w.shape
-    _need(E >= 1 and N >= 1, f"w has shape {tuple(w.shape)}")
-    _need(out_dtype in _TYPES, f"out_dtype {out_dtype} is not bf16 or fp32")
-    _need(offsets is not None or E == 1, "several experts need offsets")
+    if E < 1 or N < 1:
+        raise ValueError(f"w has shape {tuple(w.shape)}")
+    if out_dtype not in _TYPES:
+        raise ValueError(f"out_dtype {out_dtype} is not bf16 or fp32")
+    if offsets is None and E != 1:
+        raise ValueError("several experts need offsets")
     if offsets is not None:
         _offsets(offsets, "offsets", x.device)
-        _need(offsets.numel() == E + 1, f"offsets must have {E + 1} entries")
+        if offsets.numel() != E + 1:
+            raise ValueError(f"offsets must have {E + 1} entries")
     if out is None:
         out = x.new_empty((T, N), dtype=out_dtype)
     else:
         _tensor(out, "out", 2, (out_dtype,), x.device)
-        _need(tuple(out.shape) == (T, N), f"out has shape {tuple(out.shape)}")
+        if tuple(out.shape) != (T, N):
+            raise ValueError(f"out has shape {tuple(out.shape)}")
         _apart(out, "out", x=x, w=w, offsets=offsets)
     _call(tre.lib.tre_mxfp4_matmul, x.device, x.data_ptr(), x.stride(0), w.data_ptr(),
           _ptr(offsets), E, T, N, K, _TYPES[out_dtype], out.data_ptr(), out.stride(0))
@@ -226,22 +238,26 @@ def add_rmsnorm(x, delta, gain, eps: float, x_out=None, out=None):
     T, d = x.shape
     if delta is not None:
         _tensor(delta, "delta", 2, tuple(_TYPES), x.device)
-        _need(delta.shape == x.shape, f"delta has shape {tuple(delta.shape)}")
+        if delta.shape != x.shape:
+            raise ValueError(f"delta has shape {tuple(delta.shape)}")
     _tensor(gain, "gain", 1, (torch.bfloat16,), x.device)
-    _need(gain.shape[0] == d, f"gain has {gain.shape[0]} entries, not {d}")
+    if gain.shape[0] != d:
+        raise ValueError(f"gain has {gain.shape[0]} entries, not {d}")
     own_x, own = x_out is None, out is None
     if own_x:
         x_out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif x_out is not x:
         _tensor(x_out, "x_out", 2, (torch.float32,), x.device)
-        _need(x_out.shape == x.shape, f"x_out has shape {tuple(x_out.shape)}")
+        if x_out.shape != x.shape:
+            raise ValueError(f"x_out has shape {tuple(x_out.shape)}")
         if x_out.data_ptr() != x.data_ptr() or x_out.stride() != x.stride():
             _apart(x_out, "x_out", x=x)
     if own:
         out = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     else:
         _tensor(out, "out", 2, (torch.bfloat16,), x.device)
-        _need(out.shape == x.shape, f"out has shape {tuple(out.shape)}")
+        if out.shape != x.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}")
         _apart(out, "out", x=x, delta=delta, gain=gain)
     if not own_x:
         _apart(x_out, "x_out", delta=delta, gain=gain, out=None if own else out)
