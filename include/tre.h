@@ -455,8 +455,9 @@ int32_t tre_plan_op_groups(const tre_config* cfg, int32_t num_sms, int32_t smem_
  *   out[t][h] = sum_s p_s v[h / (Hq / Hkv)][s],  p = softmax_s(scale q[t][h] . k[..][s])
  * A row that sees no key (nk < nq) is written as zeros.  Rows of `out` that belong to no
  * sequence are left as they are.  Keys that a row does not see never reach it, whatever
- * they hold (NaN and infinities included); the probabilities are rounded to bf16 (a
- * relative error of at most 2^-8 each) for the product with v, their sum is not. */
+ * they hold (NaN and infinities included); a row that sees a score beyond fp32, an infinite
+ * or NaN one becomes NaN.  The probabilities are good to 2^-13 and rounded to bf16 (another
+ * 2^-8 each, relative) for the product with v, their sum is not rounded. */
 typedef struct {
   int32_t n_q_heads, n_kv_heads, head_dim;   /* Hq % Hkv == 0; head_dim 64 or 128          */
   int32_t n_seqs;                            /* sequences; 0 = one that owns every row     */
@@ -474,9 +475,11 @@ typedef struct {
  * workspace holds the parts until they are joined. */
 tre_status tre_prompt_attention_workspace(const tre_attention* a, int32_t num_sms, size_t* bytes);
 
-/* q_offsets, kv_offsets: device int32[n_seqs + 1], not decreasing (NULL with n_seqs 0).
+/* q, k, v, out bf16 by a's strides (16-byte aligned, rows and heads apart by whole 16-byte
+ * units and at least head_dim; at most 2^30 rows x heads of q, 2^30 rows of k).
+ * q_offsets, kv_offsets: device int32[n_seqs + 1], not decreasing (NULL with n_seqs 0).
  * They are read when the kernel runs, so a captured call follows their contents; entries
- * outside [0, rows] are clamped to it.  workspace (16-byte aligned, workspace_bytes as
+ * outside [0, rows] are clamped to it, a sequence whose bounds decrease is empty.  workspace (16-byte aligned, workspace_bytes as
  * reported above, NULL when 0) holds nothing before or after the call. */
 tre_status tre_prompt_attention(const tre_attention* a, const void* q, const void* k,
                                 const void* v, const int32_t* q_offsets,
@@ -523,7 +526,7 @@ tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, const void* w,
                             tre_stream stream);
 
 /* x_out = x + delta (fp32; delta may be NULL: x_out = x), out = bf16(x_out * g * r) with
- * r = 1 / sqrt(mean(x_out^2) + eps), row by row.  x, x_out fp32 [rows][d], delta
+ * r = 1 / sqrt(mean(x_out^2) + eps), row by row, the sum of squares in fp32.  x, x_out fp32 [rows][d], delta
  * [rows][d] (TRE_BF16 or TRE_F32), gain bf16[d], out bf16 [rows][d]; d a multiple of 8.
  * x_out may be x itself (the residual stream updated in place) and may be NULL. */
 tre_status tre_add_rmsnorm(const float* x, int64_t x_row_stride, const void* delta,

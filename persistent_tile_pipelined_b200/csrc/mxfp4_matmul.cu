@@ -1,14 +1,29 @@
 // Rows of activations times MXFP4 matrices, grouped by expert (declared in include/tre.h as
 // tre_mxfp4_matmul).
 //
-// out^T = W x^T on the tensor cores: 128 matrix rows are the M side, kN rows of x the N side.
-// An E2M1 number times a power of two has two significant bits, so the decoded weight is
-// exact in bf16 and the product is kind::f16 with fp32 sums; the activations keep their
-// bits.  Per stage of kKS weights the copy warp brings the codes of 128 rows and the kN rows
-// of x into shared memory; two warpgroups take stages in turn, one thread per matrix row,
-// and write the decoded weights straight into tensor memory, where the product reads its A
-// side (no second trip through shared memory, no swizzle, no proxy fence); one thread issues
-// the products.
+// out^T = W x^T on the tensor cores: 128 matrix rows are the M side, 16 to 256 rows of x the N
+// side.  An E2M1 number times a power of two has two significant bits, so the decoded weight is
+// exact in bf16 and the product is kind::f16 with fp32 sums; the activations keep their bits.
+// One warp copies the codes of 128 rows (256 weights at a time) and the rows of x to shared
+// memory; two warpgroups take steps of 64 or 128 weights in turn, one thread per matrix row, and
+// write the decoded weights straight into tensor memory, where the product reads its A side (no
+// second trip through shared memory, no swizzle, no proxy fence); one warp issues the products.
+//
+// A job is a tile of x times 128 matrix rows.  The experts' counts are known on the device only:
+// each CTA sums their tiles and finds its job.  Tiles up to 128 rows run two CTAs an SM, one job
+// each, so that one starts or ends while the other multiplies (resident CTAs: 732 us against 620
+// on the case below); the 256-row tile has the SM alone, stays, and lets two further
+// warpgroups carry the sums out (278 -> 247 us).  For few rows k is split over a cluster of up
+// to 8 CTAs, which adds the parts through distributed shared memory, in order.
+//
+// What bounds it, B200.  Few rows per expert (4096 rows over 256 experts of 2048 x 7168: 2.0 GB
+// of codes, 272 us at the measured copy rate): decoding, 600-630 us, 2.9 TB/s.  A pair of weights
+// takes three operations of the logic unit (two a clock and SM) and two multiply-adds; decoded
+// weights then pass through tensor memory at two bytes in and out.  Without the decoding's
+// arithmetic the same case takes 461 us, with a third warpgroup for it 638, with the conversion
+// instruction (e2m1 pair to f16, then to bf16) 719 against 677.  Many rows (8192 x 2048 over 4
+// experts of 7168 rows): 242-247 us, 990 TFLOP/s, 0.61 of the measured 1615; every 128 matrix
+// rows read their x again, 8.4 TB/s from L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -32,7 +47,6 @@ struct Tile {
   static constexpr int kABufs = N == 256 ? 8 : N == 128 ? 4 : 2;  // an equal number per warpgroup
   static constexpr int kACols = KS / 2;              // tensor-memory columns of one A step
   static constexpr int kCols = N == 256 ? 512 : 256;
-  static constexpr int kDBufs = N <= 64 ? 2 : 1;     // sums of two jobs
   static constexpr int kDCol = kABufs * kACols;
   static constexpr int kXBytes = N * KS * 2, kWBytes = kRows * KW / 2;
   static constexpr int kSmem = WST * kWBytes + XST * kXBytes + 1024 + 512;
@@ -44,7 +58,7 @@ struct Tile {
   static constexpr int kCopyWarp = kDecodeWarps + kOutWarps, kMmaWarp = kCopyWarp + 1;
   static constexpr int kThreads = kStay ? 640 : 320; // (whole warpgroups where registers move)
   static constexpr int kCtas = N == 256 ? 1 : 2;     // per SM
-  static_assert(kDCol + kDBufs * N <= kCols, "tensor memory");
+  static_assert(kDCol + N <= kCols, "tensor memory");
   static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory");
 };
 
@@ -182,7 +196,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
   uint64_t* a_full = x_empty + T::XST;
   uint64_t* a_empty = a_full + T::kABufs;
   uint64_t* done = a_empty + T::kABufs;
-  uint64_t* d_free = done + T::kDBufs;
+  uint64_t* d_free = done + 1;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up, lane_tiles[32], lane_last[32];
   __shared__ Job first;
@@ -270,10 +284,8 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
       mbar_init(a_full + i, 4);
       mbar_init(a_empty + i, 1);
     }
-    for (int i = 0; i < T::kDBufs; ++i) {
-      mbar_init(done + i, 1);
-      mbar_init(d_free + i, 8);
-    }
+    mbar_init(done, 1);
+    mbar_init(d_free, 8);  // a lane of each warp that carries sums out
     fence_mbar_init();
   } else if (warp == T::kCopyWarp && lane == 0) {
     tc::prefetch_map(&wmap);
@@ -297,8 +309,8 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
   const int jobs = (int)min((int64_t)lane_last[31] * row_tiles, (int64_t)p.most_jobs);
   Job job{0, 0, 0, 0};  // of the reduction at the end
   // registers where the sums have warps of their own: 640 x 96 at launch, 256 x 80 + 256 x 136 +
-  // 128 x 40 now
-  if (T::kStay && warp >= T::kCopyWarp) tc::regs_less<40>();
+  // 128 x 48 now
+  if (T::kStay && warp >= T::kCopyWarp) tc::regs_less<48>();
   if (warp == T::kCopyWarp) {
     // (the whole warp, one lane issues: see the products)
     const bool leader = tc::elect_one();
@@ -364,12 +376,12 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
     const bool leader = tc::elect_one();
     constexpr uint32_t kHi = tc::desc_hi(1024);
     const uint32_t lo0 = tc::desc_lo(smem_u32(xring), 16);
-    int xslot = 0, xphase = 0, abuf = 0, aphase = 0, dbuf = 0, dphase = 1;
+    int xslot = 0, xphase = 0, abuf = 0, aphase = 0, dphase = 1;
     bool ok = true;
     for (int n = first_job; n < jobs && ok; n = T::kStay ? n + job_step : jobs) {
       const Job j = n == first_job ? first : find_job(n);
       const uint32_t idesc = tc::idesc_bf16(kRows, max(min(N, (j.nt + 15) & ~15), 16), 0);
-      ok = tc::wait_warp(d_free + dbuf, dphase, &gave_up);
+      ok = tc::wait_warp(d_free, dphase, &gave_up);
       for (int x = 0; x < steps && ok; ++x) {
         ok = tc::wait_warp(x_full + xslot, xphase, &gave_up) &&
              tc::wait_warp(a_full + abuf, aphase, &gave_up);
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
         if (leader) {
 #pragma unroll
           for (int i = 0; i < T::KS / 16; ++i)
-            tc::mma_ts(tmem + T::kDCol + dbuf * N, at + i * 8,
+            tc::mma_ts(tmem + T::kDCol, at + i * 8,
                        tc::desc_of(lo + (i / 4) * (N * 128 / 16) + (i % 4) * 2, kHi), idesc,
                        i > 0 || x > 0);
           tc::commit(x_empty + xslot);
@@ -389,12 +401,12 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
         if (++xslot == T::XST) xslot = 0, xphase ^= 1;
         if (++abuf == T::kABufs) abuf = 0, aphase ^= 1;
       }
-      if (leader) tc::commit(done + dbuf);
+      if (leader) tc::commit(done);
       if (!ok)  // products in flight end before the tensor memory is freed
-        for (int c = 0; c < 100000 && !mbar_try_wait(done + dbuf, dphase ^ 1); ++c) {
+        for (int c = 0; c < 100000 && !mbar_try_wait(done, dphase ^ 1); ++c) {
         }
       __syncwarp();
-      if (++dbuf == T::kDBufs) dbuf = 0, dphase ^= 1;
+      dphase ^= 1;
     }
   } else if (T::kStay && warp >= kDecodeWarps) {
     // The sums of a job: thread = matrix row, warpgroup = 128 of the rows of x.  Three
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
     const uint8_t* my_codes = ring + r * (T::KW / 2);
     constexpr int kChunks = T::KS / 32;  // 16-byte chunks of a step
     bool ok = true;
-    int slot = 0, phase = 0, dbuf = 0, dphase = 0;
+    int slot = 0, phase = 0;
     int taken = 0;  // steps of the jobs so far: the A buffers go round with them
     for (int n = first_job; n < jobs && ok; n = T::kStay ? n + job_step : jobs) {
       job = n == first_job ? first : find_job(n);
@@ -492,8 +504,9 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
           const uint32_t word = kChunks == 4 ? (wg ? hi : lo) : (u ? hi : lo) >> (16 * wg);
           const int buf = step % T::kABufs;
           const uint32_t free = (step / T::kABufs & 1) ^ 1, at = lane_addr + buf * T::kACols;
-          ok = big ? decode_step<kChunks, true>(q, word, p.four, at, a_empty + buf, free, &gave_up)
-                   : decode_step<kChunks, false>(q, word, p.four, at, a_empty + buf, free, &gave_up);
+          uint64_t* place = a_empty + buf;
+          ok = big ? decode_step<kChunks, true>(q, word, p.four, at, place, free, &gave_up)
+                   : decode_step<kChunks, false>(q, word, p.four, at, place, free, &gave_up);
           if (!ok) continue;
           tc::wait_st();
           tc::fence_before();
@@ -508,13 +521,13 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
       __syncwarp();
       if (T::kStay) continue;
       // the sums: warpgroup = half of the rows of x
-      ok = ok && tc::wait_warp(done + dbuf, dphase, &gave_up);
+      ok = ok && tc::wait_warp(done, 0, &gave_up);
       if (!ok) break;
       tc::fence_after();
       Out* out = static_cast<Out*>(p.out);
       float* part = reinterpret_cast<float*>(ring);  // split along k: [N][128], ring is idle
       constexpr int kStep = N >= 64 ? 32 : 8;
-      const uint32_t d_addr = lane_addr + T::kDCol + dbuf * N;
+      const uint32_t d_addr = lane_addr + T::kDCol;
       for (int c0 = wg * (N / 2); c0 < min((wg + 1) * (N / 2), job.nt); c0 += kStep) {
         uint32_t v[kStep];
         __syncwarp();
@@ -531,10 +544,6 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
           }
         }
       }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(d_free + dbuf);
-      if (++dbuf == T::kDBufs) dbuf = 0, dphase ^= 1;
     }
   }
   tc::fence_before();
@@ -590,7 +599,8 @@ tre_status launch(const char* op, MatmulParams p, const CUtensorMap& xmap,
 }
 
 // Rows of x per tile: the least of 16 .. 256 that covers three times an expert's average (few
-// experts' weights are decoded twice), but no more than leaves the device without tiles to fill it.
+// experts' weights are then decoded twice: 770 us with 64 rows against 838 with 32 on 16 rows an
+// expert), but no more than leaves the device without tiles to fill it.
 int tile_rows(const MatmulParams& p, int sms) {
   const int64_t avg = ((int64_t)p.rows * (p.n_experts > 1 ? 3 : 1) + p.n_experts - 1) / p.n_experts;
   int best = 16;

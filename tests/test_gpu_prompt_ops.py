@@ -4,7 +4,7 @@ Tolerances, from half-step roundings (bf16 2^-8 relative, fp32 2^-24):
 
 * attention: every probability is rounded to bf16 before the product with v (2^-8 p |v|);
   the fp32 score of D products and the exponential add less than 2^-10 of p (D 2^-24 times
-  sums of |q k| scale under 2^6, exp2 to 2^-22), the output one bf16 rounding (2^-8 |o|).
+  sums of |q k| scale under 2^6, exp2 to 2^-13), the output one bf16 rounding (2^-8 |o|).
 * product: K fp32 additions in any order, counted at 2^-23 each (alignment inside the
   matrix unit may cut instead of round): K 2^-23 sum|x w|, plus the output's rounding.
 * quantiser: exact.  Norm: fp32 sums of d squares ((d + 16) 2^-24 relative), bf16 output.
