@@ -709,7 +709,10 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
   if (threadIdx.x == 0 && gave_up) atomicExch(p.status, TRE_ERR_DEP_TIMEOUT);
 }
 
-// Joins the parts of the rows of one item, a warp per row, parts in order.
+// Joins the parts of the rows of one item, a warp per row.  Lane s reads the maximum and sum of
+// part s (and s + 32, ...), so that the parts' shares are known after one wait; then the parts
+// are added in order, several loads in flight.  Starts while the last CTAs of the first kernel
+// run, and waits for them.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
   const int g = (int)p.group.d, place = quotient(blockIdx.x, p.kv_heads);
@@ -717,6 +720,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Item it = find_item(p, g, place);
   const int rr = blockIdx.y * 8 + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (rr >= it.rows) return;
   const int row = it.row0 + rr, tok0 = quotient(row, p.group);
   const int tok = it.q0 + tok0, h = kh * g + row - tok0 * g;
@@ -724,23 +728,38 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
   const int64_t at = (int64_t)tok * p.a.n_q_heads + h;
   float m = -INFINITY;
   bool seen = false;
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = lane; s < p.splits; s += 32) {
     const float2 ml = p.part_ml[s * step + at];
     seen |= ml.y != -1.f;
     m = fmaxf(m, ml.x);
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  seen = __any_sync(0xffffffffu, seen);
   constexpr int E = D / 32;
   float l = 0.f, acc[E] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * step + at];
-    if (ml.x == -INFINITY) continue;  // nothing but zeros
-    const float f = ml.x == m ? 1.f : exp2_approx(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    const float* o = p.part_o + (s * step + at) * D;
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    float share = 0.f, sum = 0.f;  // of part s0 + lane; none without a finite maximum
+    if (s0 + lane < p.splits) {
+      const float2 ml = p.part_ml[(s0 + lane) * step + at];
+      if (ml.x != -INFINITY) {
+        share = ml.x == m ? 1.f : exp2_approx(ml.x - m);
+        sum = ml.y * share;
+      }
+      if (ml.y != ml.y) sum = ml.y;
+    }
+    const int count = min(32, p.splits - s0);
+#pragma unroll 8
+    for (int s = 0; s < count; ++s) {
+      const float f = __shfl_sync(0xffffffffu, share, s);
+      l += __shfl_sync(0xffffffffu, sum, s);
+      const float* o = p.part_o + ((s0 + s) * step + at) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(o[lane + 32 * e], f, acc[e]);
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(o[lane + 32 * e], f, acc[e]);
+    }
   }
-  __nv_bfloat16* out = p.out + (int64_t)tok * p.a.out_row_stride + (int64_t)h * p.a.out_head_stride;
+  __nv_bfloat16* out =
+      p.out + (int64_t)tok * p.a.out_row_stride + (int64_t)h * p.a.out_head_stride;
 #pragma unroll
   for (int e = 0; e < E; ++e) out[lane + 32 * e] = __float2bfloat16_rn(seen ? acc[e] / l : 0.f);
 }
@@ -815,7 +834,17 @@ tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
   if (p.splits > 1) {
     const int most = (int)std::min<int64_t>(
         kItemRows, (int64_t)p.a.n_q_rows * (p.a.n_q_heads / p.a.n_kv_heads));
-    join_kernel<D><<<dim3(items, (most + 7) / 8), 256, 0, stream>>>(p);
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(items, (most + 7) / 8);
+    c.blockDim = dim3(256);
+    c.stream = stream;
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<D>, p);
+    if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
   }
   return op_launch_status(op);
 }
