@@ -16,7 +16,7 @@
 // warpgroups carry the sums out (278 -> 247 us).  For few rows k is split over a cluster of up
 // to 8 CTAs, which adds the parts through distributed shared memory, in order.
 //
-// What bounds it, B200.  Few rows per expert (4096 rows over 256 experts of 2048 x 7168: 2.0 GB
+// What bounds it, B200.  Few rows per expert (4096 rows over 256 experts of 2048 x 7168, 219 with rows: 1.7 GB
 // of codes, 272 us at the measured copy rate): decoding, 600-630 us, 2.9 TB/s.  A pair of weights
 // takes three operations of the logic unit (two a clock and SM) and two multiply-adds; decoded
 // weights then pass through tensor memory at two bytes in and out.  Without the decoding's
