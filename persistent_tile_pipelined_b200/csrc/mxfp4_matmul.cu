@@ -16,14 +16,14 @@
 // warpgroups carry the sums out (278 -> 247 us).  For few rows k is split over a cluster of up
 // to 8 CTAs, which adds the parts through distributed shared memory, in order.
 //
-// What bounds it, B200.  Few rows per expert (4096 rows over 256 experts of 2048 x 7168, 219 with rows: 1.7 GB
-// of codes, 272 us at the measured copy rate): decoding, 600-630 us, 2.9 TB/s.  A pair of weights
-// takes three operations of the logic unit (two a clock and SM) and two multiply-adds; decoded
-// weights then pass through tensor memory at two bytes in and out.  Without the decoding's
-// arithmetic the same case takes 461 us, with a third warpgroup for it 638, with the conversion
-// instruction (e2m1 pair to f16, then to bf16) 719 against 677.  Many rows (8192 x 2048 over 4
-// experts of 7168 rows): 242-247 us, 990 TFLOP/s, 0.61 of the measured 1615; every 128 matrix
-// rows read their x again, 8.4 TB/s from L2.
+// What bounds it, B200.  Few rows per expert (4096 rows over 256 experts of 2048 x 7168, 219
+// with rows: 1.7 GB of codes, 272 us at the measured copy rate): decoding, 600-630 us, 2.9 TB/s.
+// A pair of weights takes three operations of the logic unit (two a clock and SM) and two
+// multiply-adds; decoded weights then pass through tensor memory at two bytes in and out.
+// Without the decoding's arithmetic the same case takes 461 us, with a third warpgroup for it
+// 638, with the conversion instruction (e2m1 pair to f16, then to bf16) 719 against 677.  Many
+// rows (8192 x 2048 over 4 experts of 7168 rows): 242-247 us, 990 TFLOP/s, 0.61 of the measured
+// 1615; every 128 matrix rows read their x again, 8.4 TB/s from L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -577,7 +577,7 @@ tre_status launch(const char* op, MatmulParams p, const CUtensorMap& xmap,
   auto kernel = mxfp4_matmul_kernel<N, Out>;
   static std::atomic<uint64_t> devices;
   if (!allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem, &devices))
-    return op_error(TRE_ERR_CUDA, op, "the device refuses the kernel's shared memory");
+    return op_cuda_error(op, "the device refuses the kernel's shared memory");
   cudaLaunchConfig_t c = {};
   const int64_t tiles = p.offsets ? (int64_t)p.rows / N + std::min<int64_t>(p.n_experts, p.rows)
                                   : ((int64_t)p.rows + N - 1) / N;
@@ -595,7 +595,7 @@ tre_status launch(const char* op, MatmulParams p, const CUtensorMap& xmap,
   c.attrs = &attr;
   c.numAttrs = p.splits > 1 ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&c, kernel, xmap, wmap, p);
-  return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  return e == cudaSuccess ? TRE_OK : op_cuda_error(op, cudaGetErrorString(e));
 }
 
 // Rows of x per tile: the least of 16 .. 256 that covers three times an expert's average (few

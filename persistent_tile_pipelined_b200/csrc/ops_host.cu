@@ -101,7 +101,7 @@ TRE_EXPORT tre_status tre_ops_status(int32_t* device_status) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_ops_status, sizeof(v));
   if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_ops_status, &zero, sizeof(zero));
-  if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+  if (e != cudaSuccess) return op_cuda_error(op, cudaGetErrorString(e));
   *device_status = v;
   return TRE_OK;
 }

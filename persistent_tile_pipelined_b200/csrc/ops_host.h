@@ -16,6 +16,12 @@ inline tre_status op_error(tre_status st, const char* op, const std::string& wha
   return st;
 }
 
+// A failed runtime call: its error is reported here and must not be the next call's as well.
+inline tre_status op_cuda_error(const char* op, const char* what) {
+  cudaGetLastError();
+  return op_error(TRE_ERR_CUDA, op, what);
+}
+
 inline tre_status op_launch_status(const char* op) {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));

@@ -828,7 +828,7 @@ tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
   auto kernel = prompt_attention_kernel<D>;
   static std::atomic<uint64_t> devices;
   if (!allow_smem(reinterpret_cast<const void*>(kernel), Shape<D>::kSmem, &devices))
-    return op_error(TRE_ERR_CUDA, op, "the device refuses the kernel's shared memory");
+    return op_cuda_error(op, "the device refuses the kernel's shared memory");
   const unsigned items = (unsigned)(p.tiles * p.a.n_kv_heads);
   kernel<<<dim3(items, p.splits), kThreadsAttn, Shape<D>::kSmem, stream>>>(kmap, vmap, p);
   if (p.splits > 1) {
@@ -844,7 +844,7 @@ tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
     c.attrs = &early;
     c.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<D>, p);
-    if (e != cudaSuccess) return op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+    if (e != cudaSuccess) return op_cuda_error(op, cudaGetErrorString(e));
   }
   return op_launch_status(op);
 }

@@ -121,6 +121,24 @@ def test_attention_packed(hq, hkv, d, q_lens, kv_lens):
     assert (out[sum(q_lens):] == 7.0).all()
 
 
+@pytest.mark.parametrize("hq,hkv,d,nq,nk", [(300, 1, 64, 5, 140), (1026, 2, 128, 2, 300),
+                                            (257, 1, 128, 1, 1)])
+def test_attention_more_heads_than_a_tile_has_rows(hq, hkv, d, nq, nk):
+    g = gen(hq)
+    q, k, v = normal(g, nq, hq, d), normal(g, hkv, nk, d), normal(g, hkv, nk, d)
+    check_attention(ops.prompt_attention(q, k, v), q, k, v, [nq], [nk])
+
+
+def test_attention_over_many_sequences():
+    g = gen(9)
+    q_lens = [(i * 7) % 23 for i in range(150)]
+    kv_lens = [(i * 11) % 61 for i in range(150)]  # some shorter than their rows, some empty
+    q = normal(g, sum(q_lens), 6, 64)
+    k, v = normal(g, 2, sum(kv_lens), 64), normal(g, 2, sum(kv_lens), 64)
+    out = ops.prompt_attention(q, k, v, offsets(q_lens), offsets(kv_lens))
+    check_attention(out, q, k, v, q_lens, kv_lens)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_other_strides_and_scale(d):
     g = gen(5)
@@ -491,6 +509,16 @@ def test_matmul(T, E, R, K, lens, dtype):
     assert torch.equal(y, ops.mxfp4_matmul(x, w, off, dtype))
 
 
+# more experts than a lane's 32 loads cover, most of them without rows
+@pytest.mark.parametrize("T,E", [(300, 257), (2500, 1100)])
+def test_matmul_many_experts(T, E):
+    lens = [0] * E
+    for i in range(T):
+        lens[(i * 97 + i // 50) % E if i % 3 else E - 1 - i % 5] += 1
+    x, w, off = matmul_case(T, E, 40, 96, lens)
+    check_matmul(ops.mxfp4_matmul(x, w, off), x, w, lens, 96)
+
+
 # tiles of 256 rows, more of them than SMs: a CTA takes several, whose steps and copies of
 # weights end at odd places
 MANY = [(600, 1, 9000, 64, None), (1030, 4, 5100, 96, [257, 0, 513, 260]),
@@ -602,7 +630,7 @@ def test_matmul_refuses():
 
 # ---- residual addition and norm ----------------------------------------------------------------
 @pytest.mark.parametrize("T,d", [(1, 8), (1, 4096), (3, 264), (70, 7168), (2, 9000), (2, 40000),
-                                 (1500, 4104), (1100, 520)])
+                                 (1500, 4104), (1100, 520), (2, 20008), (1, 32768)])
 @pytest.mark.parametrize("delta", [None, torch.bfloat16, torch.float32], ids=str)
 def test_add_rmsnorm(T, d, delta):
     g = gen(T + d)
