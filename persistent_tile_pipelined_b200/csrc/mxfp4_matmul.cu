@@ -17,13 +17,15 @@
 // to 8 CTAs, which adds the parts through distributed shared memory, in order.
 //
 // What bounds it, B200.  Few rows per expert (4096 rows over 256 experts of 2048 x 7168, 219
-// with rows: 1.7 GB of codes, 272 us at the measured copy rate): decoding, 600-630 us, 2.9 TB/s.
-// A pair of weights takes three operations of the logic unit (two a clock and SM) and two
-// multiply-adds; decoded weights then pass through tensor memory at two bytes in and out.
-// Without the decoding's arithmetic the same case takes 461 us, with a third warpgroup for it
-// 638, with the conversion instruction (e2m1 pair to f16, then to bf16) 719 against 677.  Many
-// rows (8192 x 2048 over 4 experts of 7168 rows): 242-247 us, 990 TFLOP/s, 0.61 of the measured
-// 1615; every 128 matrix rows read their x again, 8.4 TB/s from L2.
+// with rows: 1.7 GB of codes, 272 us at the measured copy rate): decoding, 590 us, 3.0 TB/s.
+// A pair of weights takes three operations of the logic unit (half a warp a clock) and two
+// multiply-adds: 250 ns per 128 x 128 weights and SM when nothing else runs, 340 us of the case.
+// A CTA's start and end take 90 us of it, the barriers between copies, decoding and products
+// some 50 each.  Steps of 64 weights are slower than of 128 (640 us), more places for decoded
+// weights or for x change nothing, the codes read a step ahead 626, a third decoding warpgroup
+// 638, the conversion instruction (e2m1 pair to f16, then to bf16) 719 against 677.  Many rows
+// (8192 x 2048 over 4 experts of 7168 rows): 242-247 us, 990 TFLOP/s, 0.61 of the measured 1615;
+// every 128 matrix rows read their x again, 8.4 TB/s from L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -119,18 +121,18 @@ __device__ __forceinline__ void decode32(const uint4 c, uint32_t word, int at, u
   }
 }
 
-// A step's codes (16-byte chunks q) into tensor memory, 32 columns (64 weights) at a time: the
+// A step's codes (16-byte chunks q; their scales are `word` from `byte` on) into tensor memory, 32 columns (64 weights) at a time: the
 // first half is decoded before the place is waited for, the second while the first is stored.
 // By whole warps; false when the wait gave up.
 template <int kChunks, bool kBig>
-__device__ __forceinline__ bool decode_step(const uint4* q, uint32_t word, uint32_t four,
-                                            uint32_t addr, uint64_t* empty, uint32_t parity,
+__device__ __forceinline__ bool decode_step(const uint4* q, uint32_t word, int byte,
+                                            uint32_t four, uint32_t addr, uint64_t* empty, uint32_t parity,
                                             volatile int* gave_up) {
 #pragma unroll
   for (int c = 0; c < kChunks; c += 2) {
     uint32_t v[32];
-    decode32<kBig>(q[c], word, c, four, v);
-    decode32<kBig>(q[c + 1], word, c + 1, four, v + 16);
+    decode32<kBig>(q[c], word, byte + c, four, v);
+    decode32<kBig>(q[c + 1], word, byte + c + 1, four, v + 16);
     if (c == 0) {
       if (!tc::wait_warp(empty, parity, gave_up)) return false;
       tc::fence_after();
@@ -161,6 +163,15 @@ __device__ __forceinline__ float ld_cluster(uint32_t smem_addr, uint32_t rank) {
   float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -459,8 +470,11 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
     const int r = quad * 32 + lane;
     const int blocks = p.k / 32;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint8_t* my_codes = ring + r * (T::KW / 2);
     constexpr int kChunks = T::KS / 32;  // 16-byte chunks of a step
+    // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8); the warpgroup takes chunks
+    // wg * kChunks + 0 .. of every 2 kChunks
+    const uint32_t my_codes =
+        (smem_u32(ring) + r * (T::KW / 2) + (r & 7) * 16) ^ (wg * kChunks * 16);
     bool ok = true;
     int slot = 0, phase = 0;
     int taken = 0;  // steps of the jobs so far: the A buffers go round with them
@@ -468,10 +482,14 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
       job = n == first_job ? first : find_job(n);
       const int64_t row = (int64_t)job.expert * p.n + min(job.r0 + r, p.n - 1);
       const uint8_t* scales = p.w + row * p.pitch + p.k / 2;
-      // 16 scales; zero behind the row's last, where the copies bring zero codes
+      // 16 scales: two copies' worth
       auto fetch = [&](int g) {
-        if (g * 16 >= blocks) return make_uint4(0, 0, 0, 0);
-        uint4 v = *reinterpret_cast<const uint4*>(scales + g * 16);
+        return g * 16 < blocks ? *reinterpret_cast<const uint4*>(scales + g * 16)
+                               : make_uint4(0, 0, 0, 0);
+      };
+      // Of those the warpgroup's own, a word for each copy (when they are used: the load has
+      // had two copies' time); zero behind the row's last, where the copies bring zero codes.
+      auto own = [&](uint4 v, int g) {
         const int left = blocks - g * 16;
         if (left < 16) {
           auto keep = [&](int b) { return b >= 4 ? ~0u : b <= 0 ? 0u : ~0u >> (32 - 8 * b); };
@@ -480,17 +498,25 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
           v.z &= keep(left - 8);
           v.w &= keep(left - 12);
         }
-        return v;
+        if (kChunks == 4) return wg ? make_uint2(v.y, v.w) : make_uint2(v.x, v.z);
+        const uint32_t sel = wg ? 0x7632 : 0x5410;
+        return make_uint2(__byte_perm(v.x, v.y, sel), __byte_perm(v.z, v.w, sel));
       };
-      uint4 sc = fetch(k_begin / 512), next = make_uint4(0, 0, 0, 0);
+      int g = k_begin / 512;
+      uint4 next = fetch(g);
+      uint2 sc = make_uint2(0, 0);
 #pragma unroll 1
       for (int first = 0; first < steps && ok; first += T::kSteps) {  // a copy of 256 weights
         const bool odd = (first / T::kSteps) & 1;
-        if (!odd) next = fetch(k_begin / 512 + first / (2 * T::kSteps) + 1);
-        const uint32_t lo = odd ? sc.z : sc.x, hi = odd ? sc.w : sc.y;  // the copy's 8 scales
+        if (!odd) {
+          sc = own(next, g);
+          next = fetch(++g);
+        }
+        const uint32_t word = odd ? sc.y : sc.x;
         // the same way for the whole warp: its stores to tensor memory go together
-        const bool big = __any_sync(0xffffffffu, (over128(lo) | over128(hi)) != 0);
+        const bool big = __any_sync(0xffffffffu, over128(word) != 0);
         ok = tc::wait_warp(w_full + slot, phase, &gave_up);
+        const uint32_t codes = my_codes + slot * T::kWBytes;
 #pragma unroll
         for (int u = 0; u < T::kSteps / 2; ++u) {
           const int h = 2 * u + wg;
@@ -498,15 +524,15 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
           const int step = taken + first + h;
           uint4 q[kChunks];
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)  // 128-byte swizzle: chunk c of row r at c ^ (r mod 8)
-            q[c] = *reinterpret_cast<const uint4*>(my_codes + slot * T::kWBytes +
-                                                   ((h * kChunks + c) ^ (r & 7)) * 16);
-          const uint32_t word = kChunks == 4 ? (wg ? hi : lo) : (u ? hi : lo) >> (16 * wg);
+          for (int c = 0; c < kChunks; ++c)
+            q[c] = ld_shared16(codes ^ ((2 * u * kChunks + c) * 16));
           const int buf = step % T::kABufs;
           const uint32_t free = (step / T::kABufs & 1) ^ 1, at = lane_addr + buf * T::kACols;
           uint64_t* place = a_empty + buf;
-          ok = big ? decode_step<kChunks, true>(q, word, p.four, at, place, free, &gave_up)
-                   : decode_step<kChunks, false>(q, word, p.four, at, place, free, &gave_up);
+          ok = big ? decode_step<kChunks, true>(q, word, u * kChunks, p.four, at, place, free,
+                                                &gave_up)
+                   : decode_step<kChunks, false>(q, word, u * kChunks, p.four, at, place, free,
+                                                 &gave_up);
           if (!ok) continue;
           tc::wait_st();
           tc::fence_before();
@@ -515,7 +541,6 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
         }
         if (lane == 0) mbar_arrive(w_empty + slot);
         if (++slot == T::WST) slot = 0, phase ^= 1;
-        if (odd) sc = next;
       }
       taken += steps;
       __syncwarp();
