@@ -121,13 +121,13 @@ __device__ __forceinline__ void decode32(const uint4 c, uint32_t word, int at, u
   }
 }
 
-// A step's codes (16-byte chunks q; their scales are `word` from `byte` on) into tensor memory, 32 columns (64 weights) at a time: the
-// first half is decoded before the place is waited for, the second while the first is stored.
-// By whole warps; false when the wait gave up.
+// A step's codes (16-byte chunks q; their scales are `word` from `byte` on) into tensor memory,
+// 32 columns (64 weights) at a time: the first half is decoded before the place is waited for,
+// the second while the first is stored.  By whole warps; false when the wait gave up.
 template <int kChunks, bool kBig>
 __device__ __forceinline__ bool decode_step(const uint4* q, uint32_t word, int byte,
-                                            uint32_t four, uint32_t addr, uint64_t* empty, uint32_t parity,
-                                            volatile int* gave_up) {
+                                            uint32_t four, uint32_t addr, uint64_t* empty,
+                                            uint32_t parity, volatile int* gave_up) {
 #pragma unroll
   for (int c = 0; c < kChunks; c += 2) {
     uint32_t v[32];
