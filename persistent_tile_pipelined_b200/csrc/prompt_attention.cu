@@ -44,6 +44,7 @@ constexpr int kItemRows = 2 * kTile;           // rows per CTA
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kFixWarp = 10, kFixWarps = 2;
 constexpr int kThreadsAttn = 384;
 constexpr float kRaise = 8.f;                  // log2 of how far P may exceed 1
+constexpr float kFar = 67108864.f;             // 2^26, see rest_of
 
 template <int D>
 struct Shape {
@@ -74,7 +75,7 @@ struct AttnParams {
   __nv_bfloat16* out;
   const int32_t *q_offsets, *kv_offsets;
   float* part_o;       // [splits][n_q_rows * Hq][D]
-  float2* part_ml;     // [splits][n_q_rows * Hq]: maximum, sum (sum -1: no key seen)
+  float2* part_ml;     // [splits][n_q_rows * Hq]: maximum of q . k, sum (sum -1: no key seen)
   int32_t tiles;       // upper bound of the row tiles of a kv head
   int32_t splits;
   float c;             // scale * log2(e)
@@ -167,6 +168,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// A row's exponentials are relative to its maximum m (a product q . k) times c = scale log2(e).
+// fl(m c) alone is off by up to half a unit in its last place, the same for every key of the row:
+// up to kFar a factor of at most 4 that P and its sum share; from 2^31 on an overflow, or nothing
+// but zeros.  Beyond kFar the rest of the product, exact in fp32, is taken off as well.
+__device__ __forceinline__ bool is_far(float mc) { return fabsf(mc) > kFar && mc > -INFINITY; }
+
+__device__ __forceinline__ float rest_of(float m, float c) {
+  const float mc = __fmul_rn(m, c);
+  return is_far(mc) ? fmaf(m, c, -mc) : 0.f;
+}
+
+// 2^((from - to) c) as the rows' exponentials have it, from <= to; 0 when from is -infinity (no
+// score yet).  (Far maxima branch away: code that runs once waits for every line of it.)
+__device__ __forceinline__ float share_of(float from, float to, float c) {
+  const float a = __fmul_rn(from, c), b = __fmul_rn(to, c);
+  float d = a - b;
+  if (__builtin_expect(fmaxf(fabsf(a), fabsf(b)) > kFar, 0))
+    d = from == -INFINITY ? -INFINITY : d + (rest_of(from, c) - rest_of(to, c));
+  return exp2_approx(d);
+}
+
 // Where a row's result goes: the output, or its part [split] when the keys are split.
 struct RowOut {
   __nv_bfloat16* out;
@@ -204,9 +226,9 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, int split, int tok
       x = fmaf(q[e], __bfloat162float(k[at * p.a.k_row_stride + 32 * e]), x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= p.c;
-    const float mn = fmaxf(m, x), sh = mn == -INFINITY ? 0.f : mn;
-    const float old = m == mn ? 1.f : exp2_approx(m - sh), w = exp2_approx(x - sh);
+    const float mn = fmaxf(m, x), old = share_of(m, mn, p.c);
+    const float to = mn == -INFINITY ? 0.f : mn;
+    const float w = exp2_approx(fmaf(x, p.c, -__fmul_rn(to, p.c)) - rest_of(to, p.c));
 #pragma unroll
     for (int e = 0; e < E; ++e)
       acc[e] = fmaf(w, __bfloat162float(v[at * p.a.v_row_stride + 32 * e]), acc[e] * old);
@@ -515,7 +537,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
     const int sub_least = sees(it.row0 + base);
     const int step = alternate ? 2 : 1;
     const float c = p.c;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // the row's maximum (of q . k) and sum
+    float limit = -INFINITY;  // of a tile's maximum times c: above it m is looked at; NaN: always
+    float factor = c, shift = 0.f;  // exponent = what s holds * factor - shift
     bool ok = true;
     int round = 0;
     for (int i = kb + (alternate ? sub : 0); i < n_mine; i += step, ++round) {
@@ -545,16 +569,21 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           mx[y] = max3_nan(mx[y], __uint_as_float(s[x + 2 * y]), __uint_as_float(s[x + 2 * y + 1]));
-      float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * c;
+      float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], -INFINITY);
       // a NaN or an infinite score makes the row NaN (infinity less itself): by its sum, since
       // the exponentials below need not carry it
-      if (!(top < INFINITY)) l = NAN, top = m;
-      top = fmaxf(m, top);
-      if (__any_sync(0xffffffffu, top > m + kRaise || round == 0)) {
-        const float f = top == m ? 1.f : exp2_approx(m - top);
-        m = top;
+      float top_c = __fmul_rn(top, c);
+      if (!(top_c < INFINITY)) l = NAN, top = top_c = -INFINITY;
+      if (__any_sync(0xffffffffu, !(top_c <= limit) || round == 0)) {
+        top = fmaxf(m, top);
+        top_c = __fmul_rn(top, c);
+        const bool far = is_far(top_c);
+        const bool up = __any_sync(0xffffffffu, top_c > __fmul_rn(m, c) + kRaise ||
+                                                    (far && top > m) || round == 0);
+        const float f = up ? share_of(m, top, c) : 1.f;
+        if (up) m = top;
         l *= f;
-        if (round > 0) {
+        if (up && round > 0) {
           ok = tc::wait_warp(o_done + sub, (round - 1) & 1, &gave_up);
           if (!ok) break;
           tc::fence_after();
@@ -568,9 +597,21 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
             tc::tmem_st32(o_addr + x, o);
           }
         }
+        const float mc = __fmul_rn(m, c);
+        shift = m == -INFINITY ? 0.f : mc;
+        factor = c;
+        limit = fminf(mc + kRaise, kFar);
+        if (__any_sync(0xffffffffu, far)) {  // the exponents themselves
+          const float rest = rest_of(m, c);
+#pragma unroll
+          for (int x = 0; x < kTile; ++x)
+            s[x] = __float_as_uint(fmaf(__uint_as_float(s[x]), c, -shift) - rest);
+          factor = 1.f;
+          shift = 0.f;
+          limit = NAN;
+        }
       }
-      const float shift = m == -INFINITY ? 0.f : m;
-      const float2 cc = make_float2(c, c), ms = make_float2(-shift, -shift);
+      const float2 cc = make_float2(factor, factor), ms = make_float2(-shift, -shift);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int x = 0; x < kTile; x += 64) {
@@ -637,8 +678,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
           const float2 ml = other_ml[r];
           if (ml.y != -1.f) {
             const float both = fmaxf(m, ml.x);
-            f0 = m == both ? 1.f : exp2_approx(m - both);
-            f1 = ml.x == both ? 1.f : exp2_approx(ml.x - both);
+            f0 = share_of(m, both, p.c);
+            f1 = share_of(ml.x, both, p.c);
             m = both;
             l = fmaf(ml.y, f1, l * f0);
           }
@@ -743,7 +784,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
     if (s0 + lane < p.splits) {
       const float2 ml = p.part_ml[(s0 + lane) * step + at];
       if (ml.x != -INFINITY) {
-        share = ml.x == m ? 1.f : exp2_approx(ml.x - m);
+        share = share_of(ml.x, m, p.c);
         sum = ml.y * share;
       }
       if (ml.y != ml.y) sum = ml.y;

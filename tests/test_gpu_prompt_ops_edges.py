@@ -1,0 +1,132 @@
+"""The prompt operators at the ends of their ranges, against the definitions in 64 bits."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from persistent_tile_pipelined_b200 import ops, tre  # noqa: E402
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert tre.tre_ops_status() == 0
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def normal(g, *shape, dtype=torch.bfloat16, std=1.0):
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(dtype)
+
+
+# ---- attention: scores of every finite size ------------------------------------------------
+def attention_ref(q, k, v, scale):
+    """(out, sum p |v|, scores) in fp64 of one sequence: q [T, Hq, D], k, v [Hkv, S, D]."""
+    T, S, g = q.shape[0], k.shape[1], q.shape[1] // k.shape[0]
+    s = torch.einsum("thd,hsd->hts", q.double(), k.double().repeat_interleave(g, 0)) * scale
+    see = torch.arange(S, device=DEV)[None] <= torch.arange(T, device=DEV)[:, None] + S - T
+    s = s.masked_fill(~see, float("-inf"))
+    p = torch.where(see, torch.softmax(s, -1), 0.0)
+    vd = v.double().repeat_interleave(g, 0)
+    return (torch.einsum("hts,hsd->thd", p, vd), torch.einsum("hts,hsd->thd", p, vd.abs()), s)
+
+
+# The forms of the kernel: two row tiles, one that two warpgroups share, keys split over CTAs.
+FORMS = [(200, 260, 8, 2, 128), (3, 700, 4, 2, 64), (1, 9000, 8, 2, 128), (2, 5000, 4, 1, 64)]
+
+# q . k = 2^e x + 2^(e - b) j with x of a few bits and whole j, exact in fp32; e + log2(scale):
+# from ordinary scores over those whose base-2 logarithm passes 2^24 to the end of fp32.
+SIZES = [(10, 6, 1.0), (25, 23, 1.0), (25, 23, 2.0), (26, 23, 1.0), (30, 22, 1.0), (31, 22, 1.0),
+         (33, 20, 1.0), (40, 22, 1.0), (45, 22, 2.0 ** -10), (100, 22, 1.0), (125, 22, 1.0),
+         (126, 20, 2.0 ** -100)]
+
+
+def sized(g, nq, nk, hq, hkv, d, e, b, order):
+    """q, k, v with scores as above; x falls, rises or varies along the keys."""
+    top = e // 2
+    q = torch.zeros(nq, hq, d, device=DEV)
+    q[..., 0], q[..., 1] = 2.0 ** top, 2.0 ** (e - b - (e - b) // 2)
+    q[1::3] *= -1.0  # rows whose scores are all negative
+    q[2::4, :, :2] = 0.0  # rows whose scores are all zero
+    k = torch.zeros(hkv, nk, d, device=DEV)
+    x = 1.0 + torch.randint(0, 4, (hkv, nk), generator=g, device=DEV) / 4.0
+    if order == "ties":
+        x = torch.ones_like(x)
+    elif order != "any":
+        x = x.sort(-1, descending=order == "falls").values
+    j = torch.randint(-3, 4, (hkv, nk), generator=g, device=DEV).float()
+    k[..., 0] = x * 2.0 ** (e - top)
+    k[..., 1] = j * 2.0 ** ((e - b) // 2)
+    return q.bfloat16(), k.bfloat16(), normal(g, hkv, nk, d)
+
+
+@pytest.mark.parametrize("order", ["any", "rises", "falls", "ties"])
+@pytest.mark.parametrize("e,b,scale", SIZES)
+@pytest.mark.parametrize("nq,nk,hq,hkv,d", FORMS)
+def test_attention_scores_of_every_size(nq, nk, hq, hkv, d, e, b, scale, order):
+    """The scores are exact, so what is left are the roundings of ordinary ones: p's to bf16
+    (2^-8) and its exponential (2^-13; the exponent's own rounding is 2^-24 of at most 150, and
+    of 150 2^-24 for the factor scale log2(e)), the output's (2^-8)."""
+    q, k, v = sized(gen(e + nq), nq, nk, hq, hkv, d, e, b, order)
+    out = ops.prompt_attention(q, k, v, scale=scale)
+    ref, mag, _ = attention_ref(q, k, v, scale)
+    assert out.isfinite().all()
+    tol = (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * ref.abs() + 1e-30
+    err = (out.double() - ref).abs()
+    assert (err <= tol).all(), f"{int((err > tol).sum())} of {err.numel()}, {float((err / tol).max()):.3g}"
+
+
+@pytest.mark.parametrize("bad", [False, True], ids=["finite", "nan-behind"])
+@pytest.mark.parametrize("std", [2e4, 6e4, 1e9, 1e17])
+@pytest.mark.parametrize("nq,nk,hq,hkv,d", FORMS)
+def test_attention_large_random_scores(nq, nk, hq, hkv, d, std, bad):
+    """Rows whose best score leads by more than what fp32 products can be off (2^-23 a product
+    of the sum of magnitudes, on either side) and 40: the best key's value."""
+    g = gen(int(std) % 1000 + nq)
+    q, k = normal(g, nq, hq, d, std=std), normal(g, hkv, nk, d, std=std)
+    v = normal(g, hkv, nk, d)
+    scale = d ** -0.5
+    if bad:  # the last key's value spoils the last row's result, and the rows go the long way
+        v[:, -1, 3] = float("nan")
+    out = ops.prompt_attention(q, k, v, scale=scale)
+    _, _, s = attention_ref(q, k, torch.zeros_like(v), scale)
+    mag = torch.einsum("thd,hsd->hts", q.double().abs(),
+                       k.double().abs().repeat_interleave(hq // hkv, 0)) * scale
+    best, at = s.topk(2, -1)
+    lead = (best[..., 0] - best[..., 1]) > 2 * d * 2.0 ** -23 * mag.amax(-1) + 40
+    assert lead[:, :nq].float().mean() > 0.5
+    vd = v.double().repeat_interleave(hq // hkv, 0)
+    want = torch.stack([vd[h, at[h, :, 0]] for h in range(hq)], 1)  # [T, Hq, D]
+    keep = lead.t()
+    if bad:
+        keep[-1] = False
+        assert out[-1, :, 3].isnan().all()
+        out = out[:-1]
+        keep, want = keep[:-1], want[:-1]
+    assert out.isfinite().all()
+    if keep.any():
+        err = (out.double() - want).abs()[keep]
+        assert (err <= 2 * 2.0 ** -8 * want[keep].abs() + 1e-15).all()
+
+
+@pytest.mark.parametrize("e", [10, 33, 100])
+@pytest.mark.parametrize("near", [3, 7])
+def test_attention_rows_of_one_warp_with_scores_of_different_sizes(near, e):
+    """Token 71 is the first of its eight to see the second key tile: with 4 heads a kv head the
+    32 rows of a warp, which end their large rows before the small ones (near 7) or not."""
+    g = gen(e)
+    q, k, v = sized(g, 200, 257, 8, 2, 64, e, 20, "any")
+    q[near::8] = normal(g, 25, 8, 64)
+    k[..., 2:] = normal(g, 2, 257, 62)  # which the large rows do not look at
+    q[near::8, :, :2] = 0.0
+    out = ops.prompt_attention(q, k, v, scale=0.5)
+    ref, mag, _ = attention_ref(q, k, v, 0.5)
+    tol = (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * ref.abs() + 1e-30
+    assert ((out.double() - ref).abs() <= tol).all()
