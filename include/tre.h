@@ -467,7 +467,8 @@ typedef struct {
                                                 layout) or [n_kv_rows][Hkv][D]: by strides */
   int64_t v_row_stride, v_head_stride;
   int64_t out_row_stride, out_head_stride;
-  float scale;                               /* > 0; 1 / sqrt(D) in the engine's decode    */
+  float scale;                               /* > 0, 1 / sqrt(D) in the engine's decode;
+                                                scale log2(e) must not exceed fp32         */
 } tre_attention;
 
 /* Bytes of device workspace that tre_prompt_attention needs for `a` on a device of num_sms

@@ -45,6 +45,7 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9, kFixWarp = 10, kFixWarps = 2;
 constexpr int kThreadsAttn = 384;
 constexpr float kRaise = 8.f;                  // log2 of how far P may exceed 1
 constexpr float kFar = 67108864.f;             // 2^26, see rest_of
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Shape {
@@ -816,7 +817,8 @@ tre_status check(const char* op, const tre_attention* a) {
   OP_ARG((int64_t)a->n_q_rows * a->n_q_heads <= ((int64_t)1 << 30) &&
              a->n_kv_rows <= (1 << 30),
          op, "more than 2^30 rows");
-  OP_ARG(a->scale > 0.f && a->scale < 3e38f, op, "scale must be positive and finite");
+  OP_ARG(a->scale > 0.f && a->scale * kLog2e < INFINITY, op,
+         "scale must be positive and scale log2(e) finite");
   const struct {
     int64_t stride;
     int count;  // a dimension of one entry is never stepped over
@@ -948,7 +950,7 @@ TRE_EXPORT tre_status tre_prompt_attention(const tre_attention* a, const void* q
   p.part_ml = reinterpret_cast<float2*>(p.part_o + parts * a->head_dim);
   p.group = divisor(a->n_q_heads / a->n_kv_heads);
   p.kv_heads = divisor(a->n_kv_heads);
-  p.c = a->scale * 1.4426950408889634f;
+  p.c = a->scale * kLog2e;
   p.status = ops_status_ptr();
   OP_ARG(p.status, op, "the operators' status word is not available");
   OP_ARG((int64_t)p.tiles * a->n_kv_heads < ((int64_t)1 << 31), op, "too many query rows");
