@@ -10,7 +10,8 @@ Per layer, with the residual stream x in fp32 and the engine's own weights:
 
 The plain bf16 projections are library products.  Activations entering a product are bf16
 (the decode step keeps them in fp32), sums and the residual stream fp32.  A prompt may be
-run in pieces: each piece attends to what the caches already hold.
+run in pieces: each piece attends to what the caches already hold.  An application's settings
+of matrix precision and autocast do not reach in here.
 """
 from __future__ import annotations
 
@@ -26,6 +27,16 @@ def _refuse(status: int, msg: str):
 def _mm(x, w):
     """x [T][K] bf16 times w [N][K] bf16, transposed: [T][N] fp32."""
     return torch.mm(x, w.t(), out_dtype=torch.float32)
+
+
+def _mm32(x, w):
+    """x [T][K] fp32 times w [N][K] bf16, transposed, to fp32 accuracy whatever precision an
+    application allows fp32 products: x as the sum of three bf16 numbers (8 of its 24 bits
+    each), whose products with bf16 are exact in the fp32 sums."""
+    high = x.bfloat16()
+    rest = x - high
+    middle = rest.bfloat16()
+    return _mm(high, w) + (_mm(middle, w) + _mm((rest - middle).bfloat16(), w))
 
 
 def _rotary(cfg, pos: int, T: int, device):
@@ -54,7 +65,7 @@ def _experts(cfg, w, x, hn):
     E, k = cfg.n_experts, cfg.top_k
     # the router decides by order, so its input is the fp32 norm and not the bf16 one
     xn = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + cfg.norm_eps)
-    scores = torch.sigmoid((xn * w["ffn_norm"].float()) @ w["router"].float().t())
+    scores = torch.sigmoid(_mm32(xn * w["ffn_norm"].float(), w["router"].view(E, d)))
     top, idx = torch.sort(scores, dim=-1, descending=True, stable=True)  # ties: lower index
     top, idx = top[:, :k], idx[:, :k]
     weight = top / top.sum(-1, keepdim=True)
@@ -151,7 +162,7 @@ def prefill(eng, tokens, pos: int = 0, x_out=None) -> None:
         _refuse(tre.TRE_ERR_INVALID_ARG, f"a token is outside [0, {cfg.vocab})")
     if T == 0:
         return
-    with torch.cuda.device(embed.device):
+    with torch.cuda.device(embed.device), torch.autocast("cuda", enabled=False):
         x = embed.view(cfg.vocab, cfg.hidden)[tokens.to(embed.device).long()].float()
         _out(x_out, x)
         y = _run(eng, x, pos, x_out is not None)
@@ -172,6 +183,6 @@ def prefill_layers(eng, x_in, pos: int = 0, x_out=None):
     _out(x_out, x_in)
     x_out = torch.empty_like(x_in) if x_out is None else x_out
     if x_in.shape[0]:
-        with torch.cuda.device(x_in.device):
+        with torch.cuda.device(x_in.device), torch.autocast("cuda", enabled=False):
             x_out.copy_(_run(eng, x_in.contiguous(), pos, True))
     return x_out
