@@ -163,17 +163,12 @@ TRE_EXPORT tre_status tre_add_rmsnorm(const float* x, int64_t x_row_stride, cons
     threads = 1024;
   }
   const int kind = !delta ? 0 : delta_type == TRE_BF16 ? 1 : 2;
-#define LAUNCH(K, N)                                                                         \
-  if (kind == K && nv == N)                                                                  \
-    add_rmsnorm_kernel<K, N><<<(unsigned)rows, threads, 0, (cudaStream_t)stream>>>(          \
-        x, x_row_stride, delta, delta_row_stride, static_cast<const __nv_bfloat16*>(gain),   \
-        eps, d, x_out, x_out_row_stride, static_cast<__nv_bfloat16*>(out), out_row_stride)
-#define LAUNCH_N(N) LAUNCH(0, N); LAUNCH(1, N); LAUNCH(2, N)
-  LAUNCH_N(0);
-  LAUNCH_N(1);
-  LAUNCH_N(2);
-  LAUNCH_N(4);
-#undef LAUNCH_N
-#undef LAUNCH
-  return op_launch_status(op);
+#define KERNELS(N) {add_rmsnorm_kernel<0, N>, add_rmsnorm_kernel<1, N>, add_rmsnorm_kernel<2, N>}
+  static constexpr decltype(&add_rmsnorm_kernel<0, 0>) kernels[][3] = {KERNELS(0), KERNELS(1),
+                                                                       KERNELS(2), KERNELS(4)};
+#undef KERNELS
+  return op_launch(op, kernels[nv == 4 ? 3 : nv][kind], dim3((unsigned)rows), threads, 0, stream, x,
+                   x_row_stride, delta, delta_row_stride, static_cast<const __nv_bfloat16*>(gain),
+                   eps, d, x_out, x_out_row_stride, static_cast<__nv_bfloat16*>(out),
+                   out_row_stride);
 }

@@ -166,14 +166,16 @@ uint32_t inverse(int64_t d) { return d == 1 ? 0u : (uint32_t)((((uint64_t)1 << 3
 
 // Rows per launch: a launch's groups stay within 2^30, so their numbers divide in 32 bits.
 template <class Launch>
-void in_slabs(int64_t rows, int64_t groups_per_row, Launch launch) {
+tre_status in_slabs(int64_t rows, int64_t groups_per_row, Launch launch) {
   const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 30) / groups_per_row);
-  for (int64_t r = 0; r < rows; r += most) launch(r, std::min(most, rows - r));
+  tre_status st = TRE_OK;
+  for (int64_t r = 0; r < rows && st == TRE_OK; r += most) st = launch(r, std::min(most, rows - r));
+  return st;
 }
 
 template <class T>
-void quantize(const T* w, int64_t stride, int64_t rows, int64_t k, int64_t pitch, uint8_t* out,
-              cudaStream_t stream) {
+tre_status quantize(const char* op, const T* w, int64_t stride, int64_t rows, int64_t k,
+                    int64_t pitch, uint8_t* out, tre_stream stream) {
   const uint32_t per_row = (uint32_t)(k / 32), groups = (uint32_t)(rows * per_row);
   const uint32_t ctas = (groups + kGroupsPerPass - 1) / kGroupsPerPass;
   const bool wide = sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(w) & 31u) == 0 &&
@@ -181,21 +183,19 @@ void quantize(const T* w, int64_t stride, int64_t rows, int64_t k, int64_t pitch
   const bool longer = ctas >= 4 * kLongGrid;
   auto kernel = longer ? mxfp4_quantize_kernel<4, false, T> : mxfp4_quantize_kernel<1, false, T>;
   if (wide) kernel = longer ? mxfp4_quantize_kernel<4, true, T> : mxfp4_quantize_kernel<1, true, T>;
-  kernel<<<longer ? (ctas + 3) / 4 : ctas, kRowThreads, 0, stream>>>(
-      w, stride, groups, per_row, inverse(per_row), k, pitch, out);
+  return op_launch(op, kernel, dim3(longer ? (ctas + 3) / 4 : ctas), kRowThreads, 0, stream, w,
+                   stride, groups, per_row, inverse(per_row), k, pitch, out);
 }
 
 template <class T>
-void dequantize(const uint8_t* w, int64_t rows, int64_t k, int64_t pitch, T* out,
-                cudaStream_t stream) {
+tre_status dequantize(const char* op, const uint8_t* w, int64_t rows, int64_t k, int64_t pitch,
+                      T* out, tre_stream stream) {
   const uint32_t per_row = (uint32_t)(k / 32), groups = (uint32_t)(rows * per_row);
   const uint32_t ctas = (groups + kGroupsPerPass - 1) / kGroupsPerPass;
-  if (ctas >= 4 * kLongGrid)
-    mxfp4_dequantize_kernel<4><<<(ctas + 3) / 4, kRowThreads, 0, stream>>>(
-        w, groups, per_row, inverse(per_row), k, pitch, out);
-  else
-    mxfp4_dequantize_kernel<1><<<ctas, kRowThreads, 0, stream>>>(w, groups, per_row,
-                                                                 inverse(per_row), k, pitch, out);
+  const bool longer = ctas >= 4 * kLongGrid;
+  auto kernel = longer ? mxfp4_dequantize_kernel<4, T> : mxfp4_dequantize_kernel<1, T>;
+  return op_launch(op, kernel, dim3(longer ? (ctas + 3) / 4 : ctas), kRowThreads, 0, stream, w,
+                   groups, per_row, inverse(per_row), k, pitch, out);
 }
 
 tre_status check_rows(const char* op, int32_t type, int64_t rows, int64_t k) {
@@ -220,16 +220,13 @@ TRE_EXPORT tre_status tre_mxfp4_quantize(const void* w, int32_t type, int64_t ro
   OP_ARG(rows == 1 || (w_row_stride >= 0 && w_row_stride % (type == TRE_BF16 ? 8 : 4) == 0), op,
          "the row stride must be whole 16-byte units");
   const int64_t pitch = pitch_of(k);
-  in_slabs(rows, k / 32, [&](int64_t r, int64_t n) {
+  return in_slabs(rows, k / 32, [&](int64_t r, int64_t n) {
     uint8_t* o = static_cast<uint8_t*>(out) + r * pitch;
-    if (type == TRE_BF16)
-      quantize(static_cast<const __nv_bfloat16*>(w) + r * w_row_stride, w_row_stride, n, k, pitch,
-               o, (cudaStream_t)stream);
-    else
-      quantize(static_cast<const float*>(w) + r * w_row_stride, w_row_stride, n, k, pitch, o,
-               (cudaStream_t)stream);
+    return type == TRE_BF16 ? quantize(op, static_cast<const __nv_bfloat16*>(w) + r * w_row_stride,
+                                       w_row_stride, n, k, pitch, o, stream)
+                            : quantize(op, static_cast<const float*>(w) + r * w_row_stride,
+                                       w_row_stride, n, k, pitch, o, stream);
   });
-  return op_launch_status(op);
 }
 
 TRE_EXPORT tre_status tre_mxfp4_dequantize(const void* w, int64_t rows, int64_t k, int32_t type,
@@ -239,12 +236,10 @@ TRE_EXPORT tre_status tre_mxfp4_dequantize(const void* w, int64_t rows, int64_t 
   if (st != TRE_OK || rows == 0) return st;
   OP_ARG(ptr16(w) && ptr16(out), op, "NULL or misaligned pointer");
   const int64_t pitch = pitch_of(k);
-  in_slabs(rows, k / 32, [&](int64_t r, int64_t n) {
+  return in_slabs(rows, k / 32, [&](int64_t r, int64_t n) {
     const uint8_t* in = static_cast<const uint8_t*>(w) + r * pitch;
-    if (type == TRE_BF16)
-      dequantize(in, n, k, pitch, static_cast<__nv_bfloat16*>(out) + r * k, (cudaStream_t)stream);
-    else
-      dequantize(in, n, k, pitch, static_cast<float*>(out) + r * k, (cudaStream_t)stream);
+    return type == TRE_BF16
+               ? dequantize(op, in, n, k, pitch, static_cast<__nv_bfloat16*>(out) + r * k, stream)
+               : dequantize(op, in, n, k, pitch, static_cast<float*>(out) + r * k, stream);
   });
-  return op_launch_status(op);
 }

@@ -665,7 +665,7 @@ TRE_EXPORT tre_status tre_mxfp4_matmul(const void* x, int64_t x_row_stride, cons
   const int sms = device_sms();
   MatmulParams p{static_cast<const uint8_t*>(w), offsets, out, out_row_stride, pitch,
                  (int32_t)rows, (int32_t)n, (int32_t)k, n_experts, 1, 0, 4u, ops_status_ptr()};
-  OP_ARG(p.status, op, "the operators' status word is not available");
+  if (!p.status) return op_cuda_error(op, "the operators' status word is not available");
   const int tile = tile_rows(p, sms);
   if (tile <= 32) {  // few tiles: split k over a cluster until the device is busy
     const int64_t tiles = (n + kRows - 1) / kRows * ((rows + tile - 1) / tile);

@@ -11,9 +11,15 @@ namespace {
 
 constexpr int kDevices = 64;
 
+// Whether a call failed; its error must not be the next call's as well.
+bool failed(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e != cudaSuccess;
+}
+
 int current_device() {
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : -1;
+  return !failed(cudaGetDevice(&dev)) && dev >= 0 && dev < kDevices ? dev : -1;
 }
 
 }  // namespace
@@ -25,7 +31,7 @@ int32_t* ops_status_ptr() {
   int32_t* at = known[dev].load(std::memory_order_relaxed);
   if (!at) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_ops_status) != cudaSuccess) return nullptr;
+    if (failed(cudaGetSymbolAddress(&p, g_ops_status))) return nullptr;
     known[dev].store(at = static_cast<int32_t*>(p), std::memory_order_relaxed);
   }
   return at;
@@ -37,7 +43,7 @@ int device_sms() {
   if (dev < 0) return 148;
   int sms = known[dev].load(std::memory_order_relaxed);
   if (!sms) {
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 148;
+    if (failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return 148;
     known[dev].store(sms, std::memory_order_relaxed);
   }
   return sms;
@@ -47,8 +53,7 @@ bool allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* devices) {
   const int dev = current_device();
   if (dev < 0) return false;
   if (devices->load(std::memory_order_relaxed) >> dev & 1) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess)
+  if (failed(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
     return false;
   devices->fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   return true;
@@ -75,7 +80,7 @@ tre_status encode_map(const char* op, CUtensorMapDataType type, int rank, const 
                       const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
                       CUtensorMapSwizzle swizzle, CUtensorMap* out) {
   const EncodeTiledFn fn = encode_fn();
-  if (!fn) return op_error(TRE_ERR_CUDA, op, "cuTensorMapEncodeTiled is not available");
+  if (!fn) return op_cuda_error(op, "cuTensorMapEncodeTiled is not available");
   cuuint64_t d[5], st[4];
   cuuint32_t b[5], one[5];
   for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i], one[i] = 1;

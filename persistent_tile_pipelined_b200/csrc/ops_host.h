@@ -22,9 +22,19 @@ inline tre_status op_cuda_error(const char* op, const char* what) {
   return op_error(TRE_ERR_CUDA, op, what);
 }
 
-inline tre_status op_launch_status(const char* op) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? TRE_OK : op_error(TRE_ERR_CUDA, op, cudaGetErrorString(e));
+// kernel<<<grid, block, smem, stream>>>(args...) with the launch's own status: what the thread's
+// earlier calls left for cudaGetLastError is not this launch's error, and stays for whom it
+// concerns.
+template <class... Params, class... Args>
+tre_status op_launch(const char* op, void (*kernel)(Params...), dim3 grid, unsigned block,
+                     size_t smem, tre_stream stream, Args... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = (cudaStream_t)stream;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, Params(args)...);
+  return e == cudaSuccess ? TRE_OK : op_cuda_error(op, cudaGetErrorString(e));
 }
 
 inline bool ptr16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

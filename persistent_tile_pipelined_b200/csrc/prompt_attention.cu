@@ -873,8 +873,9 @@ tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
   if (!allow_smem(reinterpret_cast<const void*>(kernel), Shape<D>::kSmem, &devices))
     return op_cuda_error(op, "the device refuses the kernel's shared memory");
   const unsigned items = (unsigned)(p.tiles * p.a.n_kv_heads);
-  kernel<<<dim3(items, p.splits), kThreadsAttn, Shape<D>::kSmem, stream>>>(kmap, vmap, p);
-  if (p.splits > 1) {
+  const tre_status st = op_launch(op, kernel, dim3(items, p.splits), kThreadsAttn, Shape<D>::kSmem,
+                                  stream, kmap, vmap, p);
+  if (st == TRE_OK && p.splits > 1) {
     const int most = (int)std::min<int64_t>(
         kItemRows, (int64_t)p.a.n_q_rows * (p.a.n_q_heads / p.a.n_kv_heads));
     cudaLaunchConfig_t c = {};
@@ -889,7 +890,7 @@ tre_status launch(const char* op, const AttnParams& p, const CUtensorMap& kmap,
     const cudaError_t e = cudaLaunchKernelEx(&c, join_kernel<D>, p);
     if (e != cudaSuccess) return op_cuda_error(op, cudaGetErrorString(e));
   }
-  return op_launch_status(op);
+  return st;
 }
 
 tre_status map_of(const char* op, const void* base, int D, int64_t rows, int heads,
@@ -952,7 +953,7 @@ TRE_EXPORT tre_status tre_prompt_attention(const tre_attention* a, const void* q
   p.kv_heads = divisor(a->n_kv_heads);
   p.c = a->scale * kLog2e;
   p.status = ops_status_ptr();
-  OP_ARG(p.status, op, "the operators' status word is not available");
+  if (!p.status) return op_cuda_error(op, "the operators' status word is not available");
   OP_ARG((int64_t)p.tiles * a->n_kv_heads < ((int64_t)1 << 31), op, "too many query rows");
   CUtensorMap kmap{}, vmap{};
   if (a->n_kv_rows > 0) {

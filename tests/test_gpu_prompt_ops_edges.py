@@ -1,4 +1,6 @@
 """The prompt operators at the ends of their ranges, against the definitions in 64 bits."""
+import ctypes
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +132,34 @@ def test_attention_rows_of_one_warp_with_scores_of_different_sizes(near, e):
     ref, mag, _ = attention_ref(q, k, v, 0.5)
     tol = (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * ref.abs() + 1e-30
     assert ((out.double() - ref).abs() <= tol).all()
+
+
+# ---- errors of earlier calls -----------------------------------------------------------------
+def every_operator(g):
+    """A call of each operator, as functions."""
+    q, kv = normal(g, 5, 4, 64), normal(g, 2, 9, 64)
+    far = normal(g, 2, 9000, 64)
+    x, w = normal(g, 3, 64), normal(g, 8, 64)
+    rows = ops.mxfp4_quantize(w)
+    r, gain = normal(g, 3, 64, dtype=torch.float32), normal(g, 64)
+    return {"attention": lambda: ops.prompt_attention(q, kv, kv),
+            "split": lambda: ops.prompt_attention(q[:1], far, far),
+            "quantize": lambda: ops.mxfp4_quantize(w),
+            "dequantize": lambda: ops.mxfp4_dequantize(rows, 64),
+            "product": lambda: ops.mxfp4_matmul(x, rows),
+            "norm": lambda: ops.add_rmsnorm(r, None, gain, 1e-5)[1]}
+
+
+@pytest.mark.parametrize("op", ["attention", "split", "quantize", "dequantize", "product", "norm"])
+def test_an_earlier_error_of_the_caller_is_not_the_operators(op):
+    """The runtime keeps a thread's last failed call until it is asked for: an operator that is
+    enqueued neither reports it nor takes it from the caller."""
+    runtime = ctypes.CDLL("libcudart.so.12")  # the one that torch and libtre.so have loaded
+    call = every_operator(gen(1))[op]
+    want = call()
+    runtime.cudaGetLastError()
+    failed = runtime.cudaSetDevice(9999)  # refused on the host
+    assert failed != 0
+    got = call()
+    assert runtime.cudaGetLastError() == failed and runtime.cudaGetLastError() == 0
+    assert torch.equal(got, want)

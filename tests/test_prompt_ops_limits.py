@@ -1,5 +1,8 @@
 """Limits of the prompt operators that hold on the host (no GPU needed)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -19,3 +22,25 @@ def test_attention_scale_is_finite_in_base_2(scale, status):
                           128, scale)
     b = ctypes.c_size_t()
     assert tre.lib.tre_prompt_attention_workspace(ctypes.byref(a), 148, ctypes.byref(b)) == status
+
+
+# ---- errors of the runtime --------------------------------------------------------------------------
+def test_a_missing_device_is_an_error_of_the_runtime():
+    """In a process of its own that sees no device, so that nothing can be launched."""
+    code = """
+import sys
+sys.path.insert(0, sys.argv[1])
+from persistent_tile_pipelined_b200 import tre
+P = 1 << 20
+a = tre.tre_attention(8, 2, 128, 0, 5, 9, 8 * 128, 128, 128, 9 * 128, 128, 9 * 128, 8 * 128, 128, 0.1)
+status = [tre.tre_prompt_attention(a, P, P, P, 0, 0, P),
+          tre.tre_mxfp4_matmul(P, 64, P, 0, 1, 5, 9, 64, tre.TRE_F32, P, 9),
+          tre.tre_mxfp4_quantize(P, tre.TRE_F32, 4, 64, 64, P),
+          tre.tre_mxfp4_dequantize(P, 4, 64, tre.TRE_F32, P),
+          tre.tre_add_rmsnorm(P, 64, 0, 0, 0, P, 1e-5, 5, 64, P, 64, P, 64)]
+assert status == [tre.TRE_ERR_CUDA] * 5, status
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code, root], capture_output=True, text=True,
+                         env=dict(os.environ, CUDA_VISIBLE_DEVICES=""), timeout=120)
+    assert run.returncode == 0, run.stderr[-2000:]
