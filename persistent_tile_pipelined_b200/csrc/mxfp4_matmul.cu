@@ -374,14 +374,9 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
         }
       }
     }
-    if (!ok) {  // copies in flight land before the CTA ends
-      for (int i = max(0, x_used - T::XST); i < x_used; ++i)
-        for (int c = 0; c < 100000 && !mbar_try_wait(x_full + i % T::XST, i / T::XST & 1); ++c) {
-        }
-      for (int i = max(0, w_used - T::WST); i < w_used; ++i)
-        for (int c = 0; c < 100000 && !mbar_try_wait(w_full + i % T::WST, i / T::WST & 1); ++c) {
-        }
-    }
+    const long long since = clock64();
+    tc::settle_copies(x_full, x_used, T::XST, since);
+    tc::settle_copies(w_full, w_used, T::WST, since);
   } else if (warp == T::kMmaWarp) {
     // The whole warp runs the loop, so that what the products take is uniform; one lane issues.
     const bool leader = tc::elect_one();
@@ -413,12 +408,10 @@ __global__ void __launch_bounds__(Tile<N>::kThreads, Tile<N>::kCtas)
         if (++abuf == T::kABufs) abuf = 0, aphase ^= 1;
       }
       if (leader) tc::commit(done);
-      if (!ok)  // products in flight end before the tensor memory is freed
-        for (int c = 0; c < 100000 && !mbar_try_wait(done, dphase ^ 1); ++c) {
-        }
       __syncwarp();
       dphase ^= 1;
     }
+    if (first_job < jobs) tc::settle(done, dphase, clock64());
   } else if (T::kStay && warp >= kDecodeWarps) {
     // The sums of a job: thread = matrix row, warpgroup = 128 of the rows of x.  Three
     // quarters wait in registers so that the tensor memory is free after one is stored.

@@ -265,7 +265,7 @@ enum {
 // kAlternate: key tile i belongs to row tile (i - kb) mod 2, whose S runs two key tiles ahead of
 // its O; else both row tiles take every key tile, S one ahead.
 template <int D, bool kAlternate>
-__device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint64_t* bars,
+__device__ __forceinline__ void issue_products(uint8_t* qs, uint64_t* full, uint64_t* bars,
                                                uint32_t tmem, int kb, int ke, int n0, int n1,
                                                int least, volatile int* gave_up) {
   using T = Shape<D>;
@@ -302,11 +302,11 @@ __device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint
     if (half) tc::commit(bars + kBarO + sub);
   };
   for (int i = 0; i < min(kAhead, total); ++i) {
-    if (!arrived(2 * i)) return false;
+    if (!arrived(2 * i)) return;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       if (!takes(sub, i)) continue;
-      if (!tc::wait(bars + kBarQ + (kAlternate ? 0 : sub), 0, gave_up)) return false;
+      if (!tc::wait(bars + kBarQ + (kAlternate ? 0 : sub), 0, gave_up)) return;
       tc::fence_after();
       scores(sub, 2 * i);
     }
@@ -315,22 +315,22 @@ __device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint
   int fixed = 0;
   for (int i = 0; i < total; ++i) {
     const int nv = 2 * i + 1, next = i + kAhead, nk = 2 * next;
-    if (!arrived(nv)) return false;
+    if (!arrived(nv)) return;
     const bool partly = (kb + i + 1) * kTile > least;
     if (partly) mbar_arrive(bars + kBarCheck);
     const int round = kAlternate ? i >> 1 : i;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       if (!takes(sub, i)) continue;
-      if (!tc::wait(bars + kBarHalf + sub, round & 1, gave_up)) return false;
-      if (partly && !tc::wait(bars + kBarFixed, fixed & 1, gave_up)) return false;
+      if (!tc::wait(bars + kBarHalf + sub, round & 1, gave_up)) return;
+      if (partly && !tc::wait(bars + kBarFixed, fixed & 1, gave_up)) return;
       tc::fence_after();
       outputs(sub, nv, round > 0, 0);
-      if (!tc::wait(bars + kBarP + sub, round & 1, gave_up)) return false;
+      if (!tc::wait(bars + kBarP + sub, round & 1, gave_up)) return;
       tc::fence_after();
       outputs(sub, nv, true, 1);
       if (takes(sub, next)) {
-        if (!arrived(nk)) return false;
+        if (!arrived(nk)) return;
         scores(sub, nk);
       }
     }
@@ -338,7 +338,6 @@ __device__ __forceinline__ bool issue_products(uint8_t* qs, uint64_t* full, uint
     tc::commit(empty + nv % kPlaces);
     if (next < total) tc::commit(empty + nk % kPlaces);
   }
-  return true;
 }
 
 template <int D>
@@ -447,22 +446,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1)
           tc::load_3d(dst + h * kTile * 128, n & 1 ? &vmap : &kmap, h * 64, row, kh, full + slot);
         if (++slot == places) slot = 0, phase ^= 1;
       }
-      if (gave_up)  // copies in flight land before the CTA ends
-        for (int i = max(0, n - places); i < n; ++i)
-          for (int x = 0; x < 100000 && !mbar_try_wait(full + i % places, i / places & 1); ++x) {
-          }
+      tc::settle_copies(full, n, places, clock64());
     }
   } else if (warp == kMmaWarp) {
     if (tc::elect_one()) {
-      const bool ok = alternate ? issue_products<D, true>(qs, full, q_full, tmem, kb, ke, n_sub[0],
-                                                          n_sub[1], least, &gave_up)
-                                : issue_products<D, false>(qs, full, q_full, tmem, kb, ke,
-                                                           n_sub[0], n_sub[1], least, &gave_up);
-      if (!ok) {  // products in flight end before the tensor memory is freed
-        tc::commit(drained);
-        for (int x = 0; x < 100000 && !mbar_try_wait(drained, 0); ++x) {
-        }
-      }
+      if (alternate)
+        issue_products<D, true>(qs, full, q_full, tmem, kb, ke, n_sub[0], n_sub[1], least,
+                                &gave_up);
+      else
+        issue_products<D, false>(qs, full, q_full, tmem, kb, ke, n_sub[0], n_sub[1], least,
+                                 &gave_up);
+      tc::commit(drained);
+      tc::settle(drained, 0, clock64());
     }
   } else if (warp >= kFixWarp) {
     // Key tiles that some row sees only in part: values of keys behind the sequence become

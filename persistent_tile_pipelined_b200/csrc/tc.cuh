@@ -47,6 +47,21 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait(bar, parity, gave_up));
 }
 
+// What a CTA has issued ends before the CTA does: another role may give up after the issuing one
+// has left its loop, so both are waited for whatever has happened, and nothing is lost by it where
+// all went well (the sums that the CTA stores come after them).  Two seconds for all of them.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity, long long since) {
+  while (!mbar_try_wait(bar, parity) && clock64() - since < kWaitClocks) {
+  }
+}
+
+// `issued` copies over a ring of `places`: the last one of each place.
+__device__ __forceinline__ void settle_copies(uint64_t* full, int issued, int places,
+                                              long long since) {
+  for (int i = max(0, issued - places); i < issued; ++i)
+    settle(full + i % places, i / places & 1, since);
+}
+
 // ---- one lane of a converged warp -------------------------------------------------------
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

@@ -1,6 +1,7 @@
 """Limits of the prompt operators that hold on the host (no GPU needed)."""
 import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -44,3 +45,21 @@ assert status == [tre.TRE_ERR_CUDA] * 5, status
     run = subprocess.run([sys.executable, "-c", code, root], capture_output=True, text=True,
                          env=dict(os.environ, CUDA_VISIBLE_DEVICES=""), timeout=120)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+# ---- the end of a CTA ---------------------------------------------------------------------------
+@pytest.mark.parametrize("source", ["prompt_attention.cu", "mxfp4_matmul.cu"])
+def test_copies_and_products_end_before_the_cta_whoever_gave_up(source):
+    """The threads that issue copies and products wait for the last of them in every path: one
+    that has finished its loop cannot know that another role gives up later, after which the
+    shared and tensor memory go to another CTA.  (Read, not run: a wait that runs out beside
+    work in flight would be a fault on purpose.)"""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, source)).read())
+    calls = [m.start() for m in re.finditer(r"tc::settle(_copies)?\(", text)]
+    assert len(calls) >= 2
+    for at in calls:
+        before = text[:at].rstrip()
+        assert before.endswith((";", "}")) or before.endswith("if (first_job < jobs)"), before[-80:]
+    assert "tc::settle_copies(" in text and re.search(r"tc::settle\(", text)
+    # whole loops over the barriers of their own are not left beside them
+    assert "mbar_try_wait(" not in text
