@@ -493,6 +493,11 @@ tre_status tre_prompt_attention(const tre_attention* a, const void* q, const voi
  * it (0: every operator call so far has finished its work). */
 tre_status tre_ops_status(int32_t* device_status);
 
+/* Enqueue a kernel whose one wait is never met and gives up after `clocks` SM clocks (0 ..
+ * 4e9): the status word then holds TRE_ERR_DEP_TIMEOUT, as after an operator's own timeout.
+ * For tests of what a program does about one. */
+tre_status tre_debug_ops_timeout(int64_t clocks, tre_stream stream);
+
 /* Element types of the operators' activations and matrices. */
 enum { TRE_BF16 = 0, TRE_F32 = 1 };
 

@@ -1,5 +1,6 @@
 // What the operators share on the host: the device status word (declared in include/tre.h as
 // tre_ops_status), the device's size and tensor maps.
+#include "tc.cuh"
 #include "tensor_map.h"
 
 namespace tre {
@@ -10,6 +11,23 @@ __device__ int32_t g_ops_status;
 namespace {
 
 constexpr int kDevices = 64;
+
+// What a wait of the tensor-core operators does when it runs out of time: nothing arrives at
+// `bar`, whose second half of the warps are told by the first to give up.  No copy or product is
+// in flight.
+__global__ void __launch_bounds__(256) timeout_kernel(long long limit, int32_t* status) {
+  __shared__ uint64_t bar;
+  __shared__ int gave_up;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  tc::wait_warp(&bar, 0, &gave_up, threadIdx.x < blockDim.x / 2 ? limit : tc::kWaitClocks);
+  __syncthreads();
+  if (threadIdx.x == 0 && gave_up) atomicExch(status, TRE_ERR_DEP_TIMEOUT);
+}
 
 // Whether a call failed; its error must not be the next call's as well.
 bool failed(cudaError_t e) {
@@ -97,6 +115,14 @@ tre_status encode_map(const char* op, CUtensorMapDataType type, int rank, const 
 }  // namespace tre
 
 using namespace tre;
+
+TRE_EXPORT tre_status tre_debug_ops_timeout(int64_t clocks, tre_stream stream) {
+  static const char* op = "tre_debug_ops_timeout";
+  OP_ARG(clocks >= 0 && clocks <= tc::kWaitClocks, op, "clocks must be 0 .. 4e9");
+  int32_t* status = ops_status_ptr();
+  if (!status) return op_cuda_error(op, "the operators' status word is not available");
+  return op_launch(op, timeout_kernel, dim3(1), 256, 0, stream, clocks, status);
+}
 
 TRE_EXPORT tre_status tre_ops_status(int32_t* device_status) {
   static const char* op = "tre_ops_status";

@@ -30,12 +30,13 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gave_up,
+                                     long long limit = kWaitClocks) {
   if (try_wait_long(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
     if (try_wait_long(bar, parity)) return true;
-    if (*gave_up || clock64() - t0 > kWaitClocks) {
+    if (*gave_up || clock64() - t0 > limit) {
       *gave_up = 1;
       return false;
     }
@@ -43,8 +44,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 }
 
 // The same by a whole warp: every lane returns what all of them found.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  return __all_sync(0xffffffffu, wait(bar, parity, gave_up));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* gave_up,
+                                          long long limit = kWaitClocks) {
+  return __all_sync(0xffffffffu, wait(bar, parity, gave_up, limit));
 }
 
 // What a CTA has issued ends before the CTA does: another role may give up after the issuing one

@@ -6,6 +6,12 @@ current stream of the tensors' device.  What a C caller could get wrong too rais
 ``tre.TreError``; a tensor of another type, device or shape raises ``ValueError``.  The
 operators have no backward pass: an input that requires a gradient is refused while
 gradients are recorded.
+
+The attention and the product bound their waits on the device.  One that runs out of time
+(about two seconds: another program holds the GPU, or a fault of the kernel) leaves the
+call's outputs unspecified; no later call raises for it.  ``tre.tre_ops_status()`` waits for
+the current device, returns ``tre.TRE_ERR_DEP_TIMEOUT`` if that has happened since it was last
+asked, and 0 otherwise: ask before results are relied on.
 """
 from __future__ import annotations
 

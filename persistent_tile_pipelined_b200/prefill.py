@@ -11,7 +11,8 @@ Per layer, with the residual stream x in fp32 and the engine's own weights:
 The plain bf16 projections are library products.  Activations entering a product are bf16
 (the decode step keeps them in fp32), sums and the residual stream fp32.  A prompt may be
 run in pieces: each piece attends to what the caches already hold.  An application's settings
-of matrix precision and autocast do not reach in here.
+of matrix precision and autocast do not reach in here.  ``Engine.status()`` waits for a
+prompt and tells whether its operators have finished their work.
 """
 from __future__ import annotations
 

@@ -88,7 +88,8 @@ EXPORTED = ("tre_create", "tre_destroy", "tre_decode_step", "tre_decode_step_hos
             "tre_reset", "tre_debug_hidden", "tre_debug_trace", "tre_step_bytes",
             "tre_plan_inspect", "tre_plan_tasks", "tre_plan_op_groups", "tre_last_error",
             "tre_prompt_attention", "tre_prompt_attention_workspace", "tre_mxfp4_quantize",
-            "tre_mxfp4_dequantize", "tre_mxfp4_matmul", "tre_add_rmsnorm", "tre_ops_status")
+            "tre_mxfp4_dequantize", "tre_mxfp4_matmul", "tre_add_rmsnorm", "tre_ops_status",
+            "tre_debug_ops_timeout")
 
 
 def _load() -> ctypes.CDLL:
@@ -133,6 +134,7 @@ def _load() -> ctypes.CDLL:
     L.tre_mxfp4_matmul.argtypes = [vp, i64, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp]
     L.tre_add_rmsnorm.argtypes = [vp, i64, vp, i32, i64, vp, f32, i64, i64, vp, i64, vp, i64, vp]
     L.tre_ops_status.argtypes = [ctypes.POINTER(i32)]
+    L.tre_debug_ops_timeout.argtypes = [i64, vp]
     L.tre_last_error.argtypes = []
     L.tre_last_error.restype = ctypes.c_char_p
     for name in ("tre_create", "tre_decode_step", "tre_decode_step_host",
@@ -141,7 +143,7 @@ def _load() -> ctypes.CDLL:
                  "tre_reset", "tre_debug_hidden", "tre_debug_trace", "tre_step_bytes",
                  "tre_plan_inspect", "tre_prompt_attention", "tre_prompt_attention_workspace",
                  "tre_mxfp4_quantize", "tre_mxfp4_dequantize", "tre_mxfp4_matmul",
-                 "tre_add_rmsnorm", "tre_ops_status"):
+                 "tre_add_rmsnorm", "tre_ops_status", "tre_debug_ops_timeout"):
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -360,6 +362,10 @@ def tre_ops_status() -> int:
     return st.value
 
 
+def tre_debug_ops_timeout(clocks: int, stream: int = 0) -> int:
+    return lib.tre_debug_ops_timeout(clocks, stream or None)
+
+
 # ---- convenience ------------------------------------------------------------------------------
 def config_from_workload(wl, **overrides) -> tre_config:
     c = tre_config()
@@ -505,6 +511,8 @@ class Engine:
         if self._vc is not None:
             self.weights.v_cache = ctypes.cast(self._vc, ctypes.POINTER(ctypes.c_void_p))
         self.device = device
+        self._prompts = False   # the prompt path has run: its timeouts are the engine's too
+        self._ops_status = 0
         self.h = tre_create(cfg, self.weights, device)
 
     def close(self):
@@ -554,13 +562,16 @@ class Engine:
     def prefill(self, tokens, pos: int = 0, x_out=None) -> None:
         """Run the prompt `tokens` (a list, or an int tensor) at positions pos .. pos + T - 1
         through the stack with the prompt operators, so that the caches hold [0, pos + T);
-        see prefill.py.  A prompt's first logits come from a step of its last token."""
+        see prefill.py.  A prompt's first logits come from a step of its last token.  Enqueued:
+        status() waits for it and tells whether it has finished its work."""
         from . import prefill
+        self._prompts = True
         prefill.prefill(self, tokens, pos, x_out)
 
     def prefill_layers(self, x_in, pos: int = 0, x_out=None):
         """The same for a layers-only stack: x_out [T][d] = stack(x_in [T][d]) (fp32)."""
         from . import prefill
+        self._prompts = True
         return prefill.prefill_layers(self, x_in, pos, x_out)
 
     def set_launch_mode(self, mode: int) -> int:
@@ -585,10 +596,20 @@ class Engine:
         return tre_debug_index(self.h, layer, pos, self.cfg.index_topk)
 
     def status(self):
-        return tre_get_status(self.h)
+        """(device status, index of the task that recorded it), (0, 0) when all is well.  Once the
+        engine has run a prompt also (TRE_ERR_DEP_TIMEOUT, -1) when a wait of the prompt operators
+        on the engine's device has run out of time: the caches and outputs of that prompt are
+        then unspecified.  Waits for the device; reset() clears it."""
+        code, detail = tre_get_status(self.h)
+        if self._prompts:
+            import torch
+            with torch.cuda.device(self.device):
+                self._ops_status = self._ops_status or tre_ops_status()
+        return (self._ops_status, -1) if code == TRE_OK and self._ops_status else (code, detail)
 
     def reset(self, stream=None):
         import torch
+        self._ops_status = 0
         s = stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
         tre_reset(self.h, s)
 

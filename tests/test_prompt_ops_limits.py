@@ -63,3 +63,9 @@ def test_copies_and_products_end_before_the_cta_whoever_gave_up(source):
     assert "tc::settle_copies(" in text and re.search(r"tc::settle\(", text)
     # whole loops over the barriers of their own are not left beside them
     assert "mbar_try_wait(" not in text
+
+
+# ---- waits that run out ---------------------------------------------------------------------------
+@pytest.mark.parametrize("clocks", [-1, 4_000_000_001, 1 << 62])
+def test_a_wait_to_run_out_stays_short(clocks):
+    assert tre.tre_debug_ops_timeout(clocks) == tre.TRE_ERR_INVALID_ARG
