@@ -4,8 +4,8 @@ Each function checks its tensors, allocates what it returns with torch (on the c
 stream, so it may be captured in a CUDA graph), and enqueues the native kernel on torch's
 current stream of the tensors' device.  What a C caller could get wrong too raises
 ``tre.TreError``; a tensor of another type, device or shape raises ``ValueError``.  The
-operators have no backward pass: an input that requires a gradient is refused while
-gradients are recorded.
+operators have no derivatives: an input that requires a gradient is refused while gradients
+are recorded, one with a forward-mode gradient always.
 
 The attention and the product bound their waits on the device.  One that runs out of time
 (about two seconds: another program holds the GPU, or a fault of the kernel) leaves the
@@ -19,6 +19,7 @@ import math
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import tre
 from .synth import mxfp4_pitch
@@ -47,6 +48,10 @@ def _tensor(t, name: str, ndim: int, dtypes, device=None) -> None:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient: the operator has no backward pass")
+    # (the level first: asking a tensor costs 0.4 us, and a program without forward mode has none)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and \
+            forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} has a forward-mode gradient: the operator has no derivative")
 
 
 def _span(t) -> Tuple[int, int]:

@@ -163,3 +163,30 @@ def test_an_earlier_error_of_the_caller_is_not_the_operators(op):
     got = call()
     assert runtime.cudaGetLastError() == failed and runtime.cudaGetLastError() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("op", ["attention", "split", "quantize", "product", "norm"])
+def test_forward_mode_gradients_are_refused(op):
+    """No operator has derivatives: an input with a tangent is refused like one that requires a
+    gradient."""
+    from torch.autograd import forward_ad
+    g = gen(2)
+    q, kv = normal(g, 5, 4, 64), normal(g, 2, 9, 64)
+    far = normal(g, 2, 9000, 64)
+    x, w = normal(g, 3, 64), normal(g, 8, 64)
+    r, gain = normal(g, 3, 64, dtype=torch.float32), normal(g, 64)
+    rows = ops.mxfp4_quantize(w)
+    call, inputs = {
+        "attention": (ops.prompt_attention, (q, kv, kv)),
+        "split": (ops.prompt_attention, (q[:1], far, far)),
+        "quantize": (ops.mxfp4_quantize, (w,)),
+        "product": (lambda a: ops.mxfp4_matmul(a, rows), (x,)),
+        "norm": (lambda a, b, c: ops.add_rmsnorm(a, b, c, 1e-5), (r, x, gain))}[op]
+    with forward_ad.dual_level():
+        call(*inputs)
+        for i, t in enumerate(inputs):
+            dual = forward_ad.make_dual(t, torch.ones_like(t))
+            with pytest.raises(ValueError, match="gradient"):
+                call(*inputs[:i], dual, *inputs[i + 1:])
+    with pytest.raises(ValueError, match="gradient"):
+        torch.func.jvp(lambda a: call(a, *inputs[1:]), (inputs[0],), (inputs[0],))
