@@ -75,27 +75,48 @@ def build_synth(force: bool = False) -> str:
     return SYNTH_LIB
 
 
+def _made_with(target: str, flags) -> bool:
+    """Whether `target` was made with these flags, by the note beside it."""
+    try:
+        return open(target + ".flags").read() == "\n".join(flags)
+    except OSError:
+        return False
+
+
+def _make(cmd, target: str, flags) -> None:
+    """Run cmd, which makes `target`; the note of its flags is there only once it has."""
+    note = target + ".flags"
+    if os.path.exists(note):
+        os.remove(note)
+    subprocess.check_call(cmd)
+    with open(note, "w") as f:
+        f.write("\n".join(flags))
+
+
 def build_engine(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     srcs = [os.path.join(CSRC, s) for s in ENGINE_SOURCES]
     deps = srcs + [os.path.join(CSRC, h) for h in engine_headers()] + [
         os.path.join(INCLUDE, "tre.h")]
-    if not (force or extra_flags or _stale(ENGINE_LIB, deps)):
+    flags = [*NVCC_FLAGS, *extra_flags]
+    objdir = os.path.join(PKG, "_build")
+    linked = os.path.join(objdir, os.path.basename(ENGINE_LIB))  # its note stands with the objects
+    if not (force or extra_flags or _stale(ENGINE_LIB, deps) or not _made_with(linked, flags)):
         return ENGINE_LIB
     nvcc = _nvcc()
-    objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = []
     for s in srcs:
         obj = os.path.join(objdir, os.path.basename(s) + ".o")
         objs.append(obj)
-        if not (force or extra_flags or _stale(obj, [s] + _included(s))):
+        if not (force or extra_flags or _stale(obj, [s] + _included(s)) or
+                not _made_with(obj, flags)):
             continue
-        cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", obj]
+        cmd = [nvcc, *flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", obj]
         if verbose and s.endswith(".cu"):
             cmd += ["-Xptxas", "-v"]
-        subprocess.check_call(cmd)
-    subprocess.check_call([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs,
-                           "-o", ENGINE_LIB, "-lcudart"])
+        _make(cmd, obj, flags)
+    _make([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", ENGINE_LIB,
+           "-lcudart"], linked, flags)
     return ENGINE_LIB
 
 
