@@ -455,9 +455,13 @@ int32_t tre_plan_op_groups(const tre_config* cfg, int32_t num_sms, int32_t smem_
  *   out[t][h] = sum_s p_s v[h / (Hq / Hkv)][s],  p = softmax_s(scale q[t][h] . k[..][s])
  * A row that sees no key (nk < nq) is written as zeros.  Rows of `out` that belong to no
  * sequence are left as they are.  Keys that a row does not see never reach it, whatever
- * they hold (NaN and infinities included); a row that sees a score beyond fp32, an infinite
- * or NaN one becomes NaN.  The probabilities are good to 2^-13 and rounded to bf16 (another
- * 2^-8 each, relative) for the product with v, their sum is not rounded. */
+ * they hold (NaN and infinities included).  A row that sees a NaN score, or one whose q . k or
+ * whose multiple by log2(e) is +infinity in fp32, becomes NaN; a score of -infinity has weight
+ * 0, and a row that sees no other is NaN.  The probabilities are good to 2^-13 and rounded to
+ * bf16 (another 2^-8 each, relative) for the product with v, their sum is not rounded.
+ * A NaN or an infinity in v, at a key that a row of a block of 256 query rows (tokens x heads of
+ * a group) sees and another does not, costs time: all of the block's rows are then computed one
+ * key at a time. */
 typedef struct {
   int32_t n_q_heads, n_kv_heads, head_dim;   /* Hq % Hkv == 0; head_dim 64 or 128          */
   int32_t n_seqs;                            /* sequences; 0 = one that owns every row     */
@@ -512,7 +516,7 @@ tre_status tre_mxfp4_quantize(const void* w, int32_t type, int64_t rows, int64_t
                               int64_t w_row_stride, void* out, tre_stream stream);
 
 /* The inverse: out [rows][k] (TRE_BF16 or TRE_F32, contiguous) = the numbers that MXFP4
- * rows stand for, exact in both types (6 x 2^126 and more are infinite in both). */
+ * rows stand for, exact in both types (2^128 and more are infinite in both). */
 tre_status tre_mxfp4_dequantize(const void* w, int64_t rows, int64_t k, int32_t type, void* out,
                                 tre_stream stream);
 

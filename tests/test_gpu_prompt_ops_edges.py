@@ -190,3 +190,63 @@ def test_forward_mode_gradients_are_refused(op):
                 call(*inputs[:i], dual, *inputs[i + 1:])
     with pytest.raises(ValueError, match="gradient"):
         torch.func.jvp(lambda a: call(a, *inputs[1:]), (inputs[0],), (inputs[0],))
+
+
+# ---- attention: infinite scores -----------------------------------------------------------------
+@pytest.mark.parametrize("slow", [False, True], ids=["", "bad-value-behind"])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")], ids=str)
+@pytest.mark.parametrize("nq,nk,hq,hkv,d", FORMS)
+def test_attention_infinite_scores(nq, nk, hq, hkv, d, bad, slow):
+    """A row that sees a score of +infinity or NaN is NaN; one of -infinity has no weight."""
+    g = gen(nq + nk)
+    q, k, v = normal(g, nq, hq, d), normal(g, hkv, nk, d), normal(g, hkv, nk, d)
+    at = nk - 1 - nq // 2
+    k[:, at, 5] = bad
+    q[..., 5] = torch.where(q[..., 5] == 0, 1.0, q[..., 5])
+    if slow:  # the last key's value spoils the last row's result, and the rows go the long way
+        v[:, -1, 3] = float("nan")
+    out = ops.prompt_attention(q, k, v)
+    _, _, s = attention_ref(q, k, torch.zeros_like(v), d ** -0.5)  # [hq, nq, nk]
+    poisoned = ((s == float("inf")) | s.isnan()).any(-1).t()  # [nq, hq]
+    assert poisoned.any() or bad == -float("inf") or nq < 4
+    assert out[poisoned].isnan().all()
+    p = torch.softmax(s.masked_fill(poisoned.t()[..., None], 0.0), -1)
+    vd = v.double().repeat_interleave(hq // hkv, 0)
+    if slow:
+        assert out[-1, :, 3].isnan().all()
+        vd[:, -1, 3] = 0.0  # compared below without the last row
+    ref, mag = (torch.einsum("hts,hsd->thd", p, a) for a in (vd, vd.abs()))
+    ok = ~poisoned
+    if slow:
+        ok[-1] = False
+    tol = (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * ref.abs() + 1e-30
+    assert ((out.double() - ref).abs() <= tol)[ok].all()
+
+
+@pytest.mark.parametrize("nq,nk,hq,hkv,d", FORMS)
+def test_attention_rows_of_minus_infinite_scores_alone(nq, nk, hq, hkv, d):
+    """The definition's 0 / 0: a row that sees nothing else is NaN in every form."""
+    q = torch.ones(nq, hq, d, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(hkv, nk, d, dtype=torch.bfloat16, device=DEV)
+    k[..., 0] = -float("inf")
+    v = normal(gen(nk), hkv, nk, d)
+    assert ops.prompt_attention(q, k, v).isnan().all()
+
+
+# ---- product: the smallest weights ---------------------------------------------------------------
+@pytest.mark.parametrize("T", [1, 20, 40, 100, 300])
+def test_matmul_is_exact_with_the_smallest_scales(T):
+    """Weights below 2^-126 (numbers that bf16 holds with fewer bits) times 2^64: exact."""
+    K, R = 64, 16 * 8
+    w = torch.zeros((1, R, (K // 2 + K // 32 + 15) // 16 * 16), dtype=torch.uint8, device=DEV)
+    code = torch.arange(R, device=DEV) % 16
+    byte = torch.arange(R, device=DEV) // 16  # 0 .. 7
+    w[0, :, 3] = (code << 4).to(torch.uint8)  # element 7
+    w[0, :, K // 2] = byte.to(torch.uint8)
+    w[0, :, K // 2 + 1] = 127
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV)
+    x[:, 7] = 2.0 ** 64
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=DEV)
+    want = grid[code % 8] * torch.where(code < 8, 1.0, -1.0).double() * 2.0 ** (byte - 127.0 + 64)
+    y = ops.mxfp4_matmul(x, w).double()
+    assert (y == want[None]).all()
