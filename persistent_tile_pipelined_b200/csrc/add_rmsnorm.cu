@@ -156,6 +156,9 @@ TRE_EXPORT tre_status tre_add_rmsnorm(const float* x, int64_t x_row_stride, cons
   int threads, nv;
   if (groups <= 4 * 1024) {
     nv = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
+    // Two groups a thread where there are many long rows: 1100 rows of 7168 18.5 us against 20.5
+    // with one, of 8192 20.9 against 22.6 (8192 rows 123.0 against 121.2 and 140.0 against 137.3);
+    // 1024 rows of 512 take 4.2 us with one and 9.6 with two, 64 rows of 7168 5.2 and 5.8.
     if (rows > 1024 && groups >= 512) nv = std::max<int>(nv, 2);
     threads = (int)std::max<int64_t>(32, ((groups + nv - 1) / nv + 31) / 32 * 32);
   } else {
