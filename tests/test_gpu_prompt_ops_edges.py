@@ -250,3 +250,27 @@ def test_matmul_is_exact_with_the_smallest_scales(T):
     want = grid[code % 8] * torch.where(code < 8, 1.0, -1.0).double() * 2.0 ** (byte - 127.0 + 64)
     y = ops.mxfp4_matmul(x, w).double()
     assert (y == want[None]).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (6, 1, 64)])
+def test_attention_of_a_decode_batch(hq, hkv, d):
+    """One token of each of several sequences over caches of very different lengths, some of them
+    empty: the keys are split, and each sequence ends in another part."""
+    g = gen(hq)
+    lens = [20000, 1, 0, 129, 7000, 128]
+    q = normal(g, len(lens) + 2, hq, d)  # two rows in front that belong to no sequence
+    k, v = normal(g, sum(lens), hkv, d).transpose(0, 1), normal(g, sum(lens), hkv, d).transpose(0, 1)
+    ends = torch.tensor([0] + lens, device=DEV).cumsum(0).int()
+    rows = torch.arange(2, len(lens) + 3, device=DEV, dtype=torch.int32)
+    out = torch.full_like(q, 7.0)
+    ops.prompt_attention(q, k, v, rows, ends, out=out)
+    assert (out[:2] == 7.0).all()
+    at = 0
+    for i, n in enumerate(lens):
+        if n == 0:
+            assert (out[2 + i] == 0).all()
+            continue
+        ref, mag, _ = attention_ref(q[2 + i:3 + i], k[:, at:at + n], v[:, at:at + n], d ** -0.5)
+        tol = (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * ref.abs() + 1e-30
+        assert ((out[2 + i:3 + i].double() - ref).abs() <= tol).all()
+        at += n
