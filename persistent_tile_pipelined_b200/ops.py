@@ -172,8 +172,9 @@ def mxfp4_quantize(w, out=None):
 
 
 def _rows(w, name: str, ndim: Optional[int], K: int) -> None:
-    _tensor(w, name, w.ndim if ndim is None and isinstance(w, torch.Tensor) else ndim or 1,
-            (torch.uint8,))
+    if ndim is None:  # any number of rows' dimensions
+        ndim = max(w.ndim, 1) if isinstance(w, torch.Tensor) else 1
+    _tensor(w, name, ndim, (torch.uint8,))
     if K <= 0 or K % 32:
         raise ValueError(f"k must be a positive multiple of 32, not {K}")
     if w.shape[-1] != mxfp4_pitch(K):

@@ -69,3 +69,12 @@ def test_copies_and_products_end_before_the_cta_whoever_gave_up(source):
 @pytest.mark.parametrize("clocks", [-1, 4_000_000_001, 1 << 62])
 def test_a_wait_to_run_out_stays_short(clocks):
     assert tre.tre_debug_ops_timeout(clocks) == tre.TRE_ERR_INVALID_ARG
+
+
+# ---- arguments of the torch forms -----------------------------------------------------------------
+def test_a_tensor_without_dimensions_is_refused_like_every_other():
+    torch = pytest.importorskip("torch")
+    from persistent_tile_pipelined_b200 import ops
+    for call in (lambda t: ops.mxfp4_dequantize(t.byte(), 32), ops.mxfp4_quantize):
+        with pytest.raises(ValueError, match="dimensions|row"):
+            call(torch.tensor(1.0))
