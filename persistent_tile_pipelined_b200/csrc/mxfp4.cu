@@ -2,7 +2,7 @@
 //
 // One pass: a group of 32 weights is four lanes' loads, its scale two exchanges between them, so
 // the copy rate bounds both directions.  Measured, B200: 24 x 1999 x 7168 fp32 to rows and back to
-// bf16: 384-397 us, 6.1-6.3 TB/s (0.93-0.97 of the measured copy rate).
+// bf16: 400-404 us, 6.0 TB/s (0.92 of the measured copy rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>

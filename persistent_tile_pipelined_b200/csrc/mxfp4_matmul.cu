@@ -24,7 +24,7 @@
 // some 50 each.  Steps of 64 weights are slower than of 128 (640 us), more places for decoded
 // weights or for x change nothing, the codes read a step ahead 626, a third decoding warpgroup
 // 638, the conversion instruction (e2m1 pair to f16, then to bf16) 719 against 677.  Many rows
-// (8192 x 2048 over 4 experts of 7168 rows): 242-247 us, 990 TFLOP/s, 0.61 of the measured 1615;
+// (8192 x 2048 over 4 experts of 7168 rows): 241-245 us, 990 TFLOP/s, 0.61 of the measured 1615;
 // every 128 matrix rows read their x again, 8.4 TB/s from L2.
 #include <cuda_bf16.h>
 

@@ -21,10 +21,10 @@
 // the matrix unit, the 16384 exponentials 1024 of the special-function unit; the chain softmax ->
 // P V -> next S of a tile measures 3150 clocks for the two tiles (1040 of them waiting for S, 450
 // for the maximum, 1180 for the exponentials), an item's start and end about 13000 more.
-// Measured, B200: 8192 tokens, 32 / 8 heads of 128: 513-525 us, 1050-1070 TFLOP/s of the causal
-// half (0.65 of the measured 1615, 0.77 of the 1378 that the power cap sustains); eight packed
-// prompts of 1 to 1500 tokens, 64 / 8 heads: 162 us; one token over 131072 keys: 92 us on the
-// device, 5.8 TB/s, 0.89 of the measured copy rate.
+// Measured, B200: 8192 tokens, 32 / 8 heads of 128: 508-516 us, 1065-1080 TFLOP/s of the causal
+// half (0.67 of the measured 1615, 0.78 of the 1378 that the power cap sustains); eight packed
+// prompts of 1 to 1500 tokens, 64 / 8 heads: 160-162 us; one token over 131072 keys: 96 us (90 in a
+// graph, 6.0 TB/s, 0.91 of the measured copy rate).
 // Tried and slower: three eighths or half of the exponentials on the multiply-add units (597 and
 // 579 us against 549 with a quarter); the first half of P by the old maximum (566 against 545);
 // resident CTAs that take the next item while one ends (872 against 526).
